@@ -41,6 +41,17 @@
  *   the streaming kernels otherwise). MOE_FLAG_FP8_WEIGHTS,
  *   MOE_FLAG_PACKED_WEIGHTS or MOE_FLAG_SHARED_EXPERT with it:
  *   MOE_ERR_INVALID_ARG.
+ * - Block FP8 (MOE_FLAG_FP8_BLOCK): weights and activations are e4m3 codes with
+ *   one fp32 scale per block of 128. w_gate_up / w_down hold the codes in the
+ *   same layouts, s_gate_up [E, 2*d_ff/128, d/128] / s_down [E, d/128, d_ff/128]
+ *   the scale of each 128 x 128 block (16-byte aligned). The activations are
+ *   quantised by the library as moe_block_quant says, x before gate_up and
+ *   h = SiLU(g) * u (fp32) before down, and the products run on the FP8 tensor
+ *   cores (moe_block_gemm's arithmetic). With any other weight format,
+ *   MOE_FLAG_PACKED_WEIGHTS or MOE_FLAG_STREAM_PATH: MOE_ERR_INVALID_ARG.
+ *   moe_expert_gate_up, moe_expert_gate_up_gather and moe_expert_down, whose
+ *   h is bf16, refuse it (MOE_ERR_INVALID_ARG): moe_block_gate_up and
+ *   moe_block_down take their place.
  * - Packed bf16 weights (MOE_FLAG_PACKED_WEIGHTS): w_gate_up and w_down hold
  *   the same values rearranged by moe_pack_weights into 16 KB blocks of 128
  *   rows x 64 columns (block (e, rb, kb) = rows [128 rb, 128 rb + 128) and
@@ -110,6 +121,8 @@ extern "C" {
 #define MOE_FLAG_PACKED_WEIGHTS 0x8u /* bf16 expert weights in moe_pack_weights' layout */
 #define MOE_FLAG_SHARED_EXPERT 0x10u /* expert E of the weights is a shared expert (below) */
 #define MOE_FLAG_FP4_WEIGHTS 0x20u /* expert weights are E2M1 codes + E8M0 block-32 scales */
+
+#define MOE_FLAG_FP8_BLOCK 0x40u  /* expert weights and activations e4m3, a scale per block of 128 */
 
 /* Which expert weight moe_pack_weights rearranges. */
 #define MOE_WEIGHTS_GATE_UP 0 /* w_gate_up [E, 2*d_ff, d] */
@@ -329,6 +342,125 @@ MOE_API int moe_selftest_bounded_wait(void* ws, unsigned long long limit_ns, voi
 MOE_API int moe_route_noalloc(const moe_config* cfg, const void* x, const void* w_gate,
                               const float* gate_bias, int32_t* topk_idx, float* topk_w,
                               void* stream);
+
+/* A score function of moe_select, moe_route4 and moe_forward4 only. */
+#define MOE_SCORE_SOFTMAX 2 /* s = softmax of the token's E logits */
+
+/* How a group of experts is scored (moe_group_options.group_score). */
+#define MOE_GROUP_MAX 0  /* its largest choice value */
+#define MOE_GROUP_TOP2 1 /* the sum of its two largest choice values */
+
+/* The choice of experts in groups: the E experts form n_group groups of
+ * E / n_group consecutive experts, the topk_group groups with the largest score
+ * stay (equal scores -> lower group), and the k experts are chosen among
+ * theirs. n_group = topk_group = 1 is the choice among all experts.
+ * renormalize: 1 divides the chosen scores by their sum, 0 does not. Needs
+ * n_group dividing E, 1 <= topk_group <= n_group, topk_group * E / n_group >= k
+ * and, with MOE_GROUP_TOP2, at least two experts a group (else
+ * MOE_ERR_UNSUPPORTED_SHAPE); any other group_score or renormalize is
+ * MOE_ERR_INVALID_ARG. */
+typedef struct moe_group_options {
+    int32_t n_group;
+    int32_t topk_group;
+    int32_t group_score;
+    int32_t renormalize;
+} moe_group_options;
+
+/* The choice from logits the caller has: logits [T, E] fp32, row t at
+ * logits + t * ld (ld >= E; 4-byte aligned). Of cfg only T, E, k and scale
+ * matter (d and d_ff still have to be valid). opt (NULL: sigmoid, no bias)
+ * gives score_fn and score_bias; its norm_weight must be NULL. grp NULL: no
+ * groups, renormalised. Per token:
+ *   s_e = the score of logit z_e (softmax over all E logits);
+ *   c_e = s_e + score_bias[e], or s_e without a bias: the choice value;
+ *   groups as moe_group_options says; the k largest c_e of the groups kept,
+ *   equal values -> lower index, in descending order of c;
+ *   w_j = scale * s_j / sum of the chosen s (0 where that sum is 0), or
+ *   scale * s_j without renormalize.
+ * Values are ranked by the exact c: fp32 evaluations closer than their error
+ * bound are repeated in fp64. A logit of -infinity (an expert that is out) or
+ * NaN has s = 0 and c = -infinity, bias or not: it is chosen only where fewer
+ * than k others are left; +infinity counts as the largest finite float, a NaN
+ * bias as -infinity. */
+MOE_API int moe_select(const moe_config* cfg, const float* logits, int64_t ld,
+                       const moe_route_options* opt, const moe_group_options* grp,
+                       int32_t* topk_idx, float* topk_w, void* stream);
+
+/* moe_route3 and moe_forward3 with moe_select's choice on the router's logits
+ * (after gate_bias and route_norm): softmax scores, groups and unnormalised
+ * weights. opt and grp nullable. */
+MOE_API int moe_route4(const moe_config* cfg, const void* x, const void* w_gate,
+               const float* gate_bias, const moe_route_options* opt,
+               const moe_group_options* grp, int32_t* topk_idx, float* topk_w, void* ws,
+               size_t ws_bytes, void* stream);
+MOE_API int moe_forward4(const moe_config* cfg, const void* x, const void* w_gate,
+                 const float* gate_bias, const moe_route_options* opt,
+                 const moe_group_options* grp, const void* w_gate_up, const void* s_gate_up,
+                 const void* w_down, const void* s_down, void* out, void* ws, size_t ws_bytes,
+                 void* stream);
+
+/* The layer after its router, for a routing the caller has (moe_select's, or
+ * any): group, gate_up, down, combine, in every weight format. topk_idx [T, k],
+ * topk_w [T, k]; a slot whose index is outside [0, E) adds nothing, an index
+ * may occur twice in a row. Resets the workspace status word first. */
+MOE_API int moe_forward_routed(const moe_config* cfg, const void* x, const int32_t* topk_idx,
+                       const float* topk_w, const void* w_gate_up, const void* s_gate_up,
+                       const void* w_down, const void* s_down, void* out, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* Quantise rows in blocks of 128 columns: x [M, K] bf16, row m at x + m * ldx
+ * elements (ldx >= K); codes [M, K] e4m3 and scales [M, ceil(K/128)] fp32,
+ * contiguous. With a the largest magnitude of the block's columns,
+ *   scale = a / 448 (1 where a = 0),  code = e4m3( (448 x) / a ),
+ * both in fp32 with round-to-nearest-even: for bf16 x the code is the exact
+ * quotient's rounding. An infinity or NaN in a block makes its scale
+ * infinite or NaN, and with it every product the block takes part in. K, ldx
+ * multiples of 16, x and codes 16-byte aligned; M = 0 does nothing. */
+MOE_API int moe_block_quant(const void* x, int64_t ldx, int32_t M, int32_t K, void* codes,
+                            float* scales, void* stream);
+
+/* Element types of moe_block_gemm's output. */
+#define MOE_OUT_BF16 0
+#define MOE_OUT_F32 1
+
+/* FP8 matrix product with a scale per block of 128:
+ *   out[m, n] = sum_b sx[m, b] * sw[n / 128, b] * sum_{c in block b} xq[m, c] * wq[n, c]
+ * with the blocks b of 128 consecutive columns c, everything in fp32, rounded
+ * once to out's type. xq [M, K] e4m3, sx [M, ceil(K/128)] (moe_block_quant's
+ * output); wq [N, K] e4m3, sw [ceil(N/128), ceil(K/128)]; out [M, N].
+ * Grouped: offsets [G+1] int32 on the device, non-decreasing, within [0, M]
+ * (values outside are clamped): rows [offsets[g], offsets[g+1]) take the
+ * weight g of wq [G, N, K] and sw [G, ceil(N/128), ceil(K/128)]; rows of no
+ * group are not written. offsets NULL: G must be 1 and takes all rows.
+ * K a multiple of 16 (any N >= 1, M >= 0), 1 <= G <= 256, M <= 2^24, N and
+ * K <= 2^17, G * N < 2^31; xq, wq and out 16-byte aligned. ws: a device
+ * workspace of moe_block_workspace_size bytes, 256-byte aligned, zeroed once
+ * before its first use; its first word is a status word (moe_read_status).
+ * Calls that may overlap need one each. */
+MOE_API int moe_block_gemm(const void* xq, const float* sx, const void* wq, const float* sw,
+                           const int32_t* offsets, int32_t G, int32_t M, int32_t N, int32_t K,
+                           void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                           void* stream);
+/* 0 if moe_block_gemm refuses the sizes. */
+MOE_API size_t moe_block_workspace_size(int32_t G, int32_t M, int32_t N, int32_t K);
+
+/* The steps of a block-FP8 layer (cfg with MOE_FLAG_FP8_BLOCK).
+ * moe_block_permute: quantise every token of x once (moe_block_quant) and write
+ * it to its grouped rows: xq [T*k, d] and sx [T*k, d/128] at row_of[t*k + j]
+ * (entries outside [0, T*k) are skipped; T*(k+1) rows with a shared expert). */
+MOE_API int moe_block_permute(const moe_config* cfg, const void* x, const int32_t* row_of,
+                              void* xq, float* sx, void* stream);
+/* moe_block_gate_up: hq [T*k, d_ff] e4m3 and sh [T*k, d_ff/128], the
+ * quantisation of h = SiLU(g) * u (fp32), g and u moe_block_gemm's products
+ * with the gate and the up rows. */
+MOE_API int moe_block_gate_up(const moe_config* cfg, const void* xq, const float* sx,
+                              const int32_t* offsets, const void* w_gate_up,
+                              const void* s_gate_up, void* hq, float* sh, void* ws,
+                              size_t ws_bytes, void* stream);
+/* moe_block_down: y [T*k, d] bf16, moe_block_gemm's product with w_down. */
+MOE_API int moe_block_down(const moe_config* cfg, const void* hq, const float* sh,
+                           const int32_t* offsets, const void* w_down, const void* s_down,
+                           void* y, void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise stream, then read and clear the workspace status word: MOE_OK,
  * or MOE_ERR_TIMEOUT if a bounded device wait gave up since the last read. */

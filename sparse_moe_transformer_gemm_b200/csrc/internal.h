@@ -124,15 +124,20 @@ inline WsLayout ws_layout(const moe_config& c) {
 }
 
 // ---- launchers (each returns cudaError_t of the launch) ----
+// The routers with logits_only / logits_out write the finished logits [T, E]
+// (bias and norm applied; launch_router's into the first T*E floats of logits)
+// instead of choosing.
 cudaError_t launch_router(const moe_config& c, const void* x, const void* w_gate,
                           const float* gate_bias, const float* score_bias, const float* norm_w,
                           float norm_eps, int score_fn, int32_t* idx, float* w, float* logits,
-                          float* sumsq, int32_t* counters, int ksplit, cudaStream_t s);
+                          float* sumsq, int32_t* counters, int ksplit, bool logits_only,
+                          cudaStream_t s);
 
 bool router_tc_supported(const moe_config& c);
 cudaError_t launch_router_tc(const moe_config& c, const void* x, const void* w_gate,
                              const float* gate_bias, const float* score_bias, int score_fn,
-                             int32_t* idx, float* w, int* status, cudaStream_t s);
+                             int32_t* idx, float* w, float* logits_out, int* status,
+                             cudaStream_t s);
 
 cudaError_t launch_permute(const moe_config& c, const int32_t* idx, const void* x, int32_t* counts,
                            int32_t* offsets, int32_t* row_of, void* x_perm, int32_t* hist,
@@ -189,6 +194,34 @@ cudaError_t launch_gate_up_gemm_pair_fp4(const moe_config& c, const void* x_perm
 cudaError_t launch_down_gemm_pair_fp4(const moe_config& c, const void* h, const int32_t* offsets,
                                       const void* w_down, const void* s_down, void* y,
                                       int* status, cudaStream_t s);
+
+// The choice of experts from logits [T, E] (row stride ld): select.cu.
+cudaError_t launch_select(const moe_config& c, const float* logits, long ld,
+                          const float* score_bias, int score_fn, const moe_group_options& grp,
+                          int32_t* idx, float* w, cudaStream_t s);
+
+// FP8 with a scale per block of 128: block_quant.cu, block_gemm.cu.
+cudaError_t launch_block_quant(const void* x, long ldx, int M, int K, void* codes, float* scales,
+                               cudaStream_t s);
+cudaError_t launch_block_permute(const void* x, const int32_t* row_of, int T, int kk, int d,
+                                 long R, void* codes, float* scales, cudaStream_t s);
+// A grouped product; rows past offsets[G] are not written. offsets NULL: one
+// group of all M rows. gate_up: N = d_ff output features, the weights hold
+// 2 * N rows (gate, up) and the output is hq [M, N] codes with sh [M, N/128].
+struct BlockGemm {
+    const void* xq;
+    const float* sx;
+    const void* wq;
+    const float* sw;
+    const int32_t* offsets;
+    int G, M, N, K;
+    void* out;
+    float* out_scales;  // gate_up only
+    int out_type;       // MOE_OUT_*, not for gate_up
+    int* status;
+};
+cudaError_t launch_block_gemm(const BlockGemm& p, cudaStream_t s);
+cudaError_t launch_block_gate_up(const BlockGemm& p, cudaStream_t s);
 
 cudaError_t launch_combine(const moe_config& c, const void* y, const int32_t* row_of,
                            const float* topk_w, void* out, cudaStream_t s);

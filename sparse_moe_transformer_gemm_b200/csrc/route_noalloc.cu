@@ -92,7 +92,7 @@ extern "C" int moe_route_noalloc(const moe_config* cfg, const void* x, const voi
     float* logits = reinterpret_cast<float*>(static_cast<char*>(base) + counter_bytes);
     if (cudaMemsetAsync(counters, 0, counter_bytes, s) != cudaSuccess) return MOE_ERR_CUDA;
     return moe::launch_router(*cfg, x, w_gate, gate_bias, nullptr, nullptr, 0.f, 0, topk_idx,
-                              topk_w, logits, nullptr, counters, ksplit, s) == cudaSuccess
+                              topk_w, logits, nullptr, counters, ksplit, false, s) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

@@ -48,7 +48,8 @@ router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restri
               const float* __restrict__ bias, const float* __restrict__ sbias,
               const float* __restrict__ norm_w, float norm_eps, int score_fn, int T, int d,
               int E, int k, float scale, float* __restrict__ logits, float* __restrict__ sumsq,
-              int* __restrict__ counters, int* __restrict__ idx_out, float* __restrict__ w_out) {
+              int* __restrict__ counters, int* __restrict__ idx_out, float* __restrict__ w_out,
+              int logits_only) {
     pdl_launch_and_wait();
     __shared__ __align__(16) float xs[RT][KC];
     __shared__ int s_last;
@@ -189,7 +190,13 @@ router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restri
                 sc[q] = -INFINITY;
             }
         }
-        if (sbias) {
+        if (logits_only) {
+            // every slice of this token has been read, by the same thread that
+            // overwrites the first one
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (lane + 32 * q < E) logits[(size_t)t * E + lane + 32 * q] = sc[q];
+        } else if (sbias) {
             // e_score_correction_bias: the choice ranks sigmoid + bias, the
             // weights renormalise the sigmoid scores of the chosen experts
             float prob[8];
@@ -214,12 +221,14 @@ router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restri
 cudaError_t launch_router(const moe_config& c, const void* x, const void* w_gate,
                           const float* gate_bias, const float* score_bias, const float* norm_w,
                           float norm_eps, int score_fn, int32_t* idx, float* w, float* logits,
-                          float* sumsq, int32_t* counters, int ksplit, cudaStream_t s) {
+                          float* sumsq, int32_t* counters, int ksplit, bool logits_only,
+                          cudaStream_t s) {
     dim3 grid((c.E + RE - 1) / RE, n_router_groups(c), ksplit);
     const cudaError_t err = launch_pdl(
         router_kernel, grid, dim3(RWARPS * 32), 0, s, static_cast<const __nv_bfloat16*>(x),
         static_cast<const __nv_bfloat16*>(w_gate), gate_bias, score_bias, norm_w, norm_eps, score_fn,
-        c.T, c.d, c.E, c.k, c.scale, logits, sumsq, counters, idx, w);
+        c.T, c.d, c.E, c.k, c.scale, logits, sumsq, counters, idx, w,
+        (int)logits_only);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -212,7 +212,8 @@ router_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                  const float* __restrict__ bias, const float* __restrict__ sbias, int T,
                  int d, int E, int k, int n_pad,
                  float scale, int score_fn, int* __restrict__ idx_out,
-                 float* __restrict__ w_out, int* __restrict__ status) {
+                 float* __restrict__ w_out, float* __restrict__ logits_out,
+                 int* __restrict__ status) {
     pdl_launch_and_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -382,7 +383,15 @@ router_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
     } else {
         __syncthreads();
     }
-    if (warp >= 2) {
+    if (logits_out) {
+        // the finished logits of this CTA's rows, for a choice made elsewhere
+        if (warp >= 2)
+            for (int i = threadIdx.x - 64; i < ROWS * E; i += 128) {
+                const int rr = split * ROWS + i / E, e = i % E;
+                const long t = (long)tile * BM + rr;
+                if (t < T) logits_out[t * E + e] = red[rr * es + e] + c.bias[e];
+            }
+    } else if (warp >= 2) {
         // S lanes per token row of this CTA's slice (ROWS * S = 128 threads)
         const int tid = threadIdx.x - 64;
         const int rr = tid / S, part = tid % S;
@@ -450,7 +459,7 @@ namespace {
 template <int S>
 cudaError_t launch_s(dim3 grid, const CUtensorMap& mx, const CUtensorMap& mw, const moe_config& c,
                      int n_pad, const float* gate_bias, const float* score_bias, int score_fn,
-                     int32_t* idx, float* w, int* status, cudaStream_t s) {
+                     int32_t* idx, float* w, float* logits_out, int* status, cudaStream_t s) {
     cudaError_t err = cudaFuncSetAttribute(router_tc_kernel<S>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (err != cudaSuccess) return err;
@@ -469,14 +478,15 @@ cudaError_t launch_s(dim3 grid, const CUtensorMap& mx, const CUtensorMap& mw, co
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, router_tc_kernel<S>, mx, mw, gate_bias, score_bias, c.T, c.d,
-                              c.E, c.k, n_pad, c.scale, score_fn, idx, w, status);
+                              c.E, c.k, n_pad, c.scale, score_fn, idx, w, logits_out, status);
 }
 
 }  // namespace
 
 cudaError_t launch_router_tc(const moe_config& c, const void* x, const void* w_gate,
                              const float* gate_bias, const float* score_bias, int score_fn,
-                             int32_t* idx, float* w, int* status, cudaStream_t s) {
+                             int32_t* idx, float* w, float* logits_out, int* status,
+                             cudaStream_t s) {
     const int tiles = (c.T + BM - 1) / BM;
     const int S = router_splits(c.T, c.d);
     const int n_pad = (c.E + 15) & ~15;
@@ -488,19 +498,19 @@ cudaError_t launch_router_tc(const moe_config& c, const void* x, const void* w_g
     switch (S) {
         case 1:
             err = launch_s<1>(grid, mx, mw, c, n_pad, gate_bias, score_bias, score_fn, idx, w,
-                               status, s);
+                               logits_out, status, s);
             break;
         case 2:
             err = launch_s<2>(grid, mx, mw, c, n_pad, gate_bias, score_bias, score_fn, idx, w,
-                               status, s);
+                               logits_out, status, s);
             break;
         case 4:
             err = launch_s<4>(grid, mx, mw, c, n_pad, gate_bias, score_bias, score_fn, idx, w,
-                               status, s);
+                               logits_out, status, s);
             break;
         default:
             err = launch_s<8>(grid, mx, mw, c, n_pad, gate_bias, score_bias, score_fn, idx, w,
-                               status, s);
+                               logits_out, status, s);
             break;
     }
     if (err != cudaSuccess) return err;

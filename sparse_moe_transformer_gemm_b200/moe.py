@@ -32,18 +32,29 @@ MOE_FLAG_GEMM_PATH = 0x4
 MOE_FLAG_PACKED_WEIGHTS = 0x8
 MOE_FLAG_SHARED_EXPERT = 0x10
 MOE_FLAG_FP4_WEIGHTS = 0x20
+MOE_FLAG_FP8_BLOCK = 0x40
 MOE_WEIGHTS_GATE_UP = 0
 MOE_WEIGHTS_DOWN = 1
 MOE_SCORE_SIGMOID = 0
 MOE_SCORE_SQRT_SOFTPLUS = 1
-SCORE_FNS = {"sigmoid": MOE_SCORE_SIGMOID, "sqrtsoftplus": MOE_SCORE_SQRT_SOFTPLUS}
+MOE_SCORE_SOFTMAX = 2  # moe_select, moe_route4 and moe_forward4 only
+SCORE_FNS = {"sigmoid": MOE_SCORE_SIGMOID, "sqrtsoftplus": MOE_SCORE_SQRT_SOFTPLUS,
+             "softmax": MOE_SCORE_SOFTMAX}
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
+MOE_OUT_BF16 = 0
+MOE_OUT_F32 = 1
 
 EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_permute",
             "moe_permute_index", "moe_expert_gate_up", "moe_expert_gate_up_gather",
             "moe_expert_down", "moe_experts", "moe_combine", "moe_forward", "moe_read_status",
             "moe_status_string", "moe_route_noalloc", "moe_pack_weights", "moe_route2",
             "moe_forward2", "moe_route3", "moe_forward3", "moe_selftest_bounded_wait",
-            "moe_ep_row_experts")
+            "moe_ep_row_experts", "moe_select", "moe_route4", "moe_forward4",
+            "moe_forward_routed", "moe_block_quant", "moe_block_gemm",
+            "moe_block_workspace_size", "moe_block_permute", "moe_block_gate_up",
+            "moe_block_down")
 
 MOE_NOALLOC_SCRATCH_BYTES = 2 << 20
 MOE_EP_MAX_SEGMENTS = 8192
@@ -71,11 +82,25 @@ class MoeRouteOptions(ctypes.Structure):
 
 def route_options(score_bias=None, norm_weight=None, norm_eps: float = 1e-6,
                   score_fn: str = "sigmoid"):
-    """Router options; score_fn is "sigmoid" or "sqrtsoftplus" (or a MOE_SCORE_* value)."""
+    """Router options; score_fn is "sigmoid", "sqrtsoftplus" or, for moe_select, moe_route4
+    and moe_forward4, "softmax" (or a MOE_SCORE_* value)."""
     fn = SCORE_FNS[score_fn] if isinstance(score_fn, str) else int(score_fn)
     return MoeRouteOptions(None if score_bias is None else score_bias.data_ptr(),
                            None if norm_weight is None else norm_weight.data_ptr(),
                            float(norm_eps), fn)
+
+
+class MoeGroupOptions(ctypes.Structure):
+    """moe_group_options: n_group, topk_group, group_score (MOE_GROUP_*), renormalize."""
+    _fields_ = [("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
+
+
+def group_options(n_group: int = 1, topk_group: int = 1, group_score: str = "max",
+                  renormalize: bool = True):
+    """The choice in groups; group_score is "max" or "top2" (or a MOE_GROUP_* value)."""
+    gs = GROUP_SCORES[group_score] if isinstance(group_score, str) else int(group_score)
+    return MoeGroupOptions(int(n_group), int(topk_group), gs, int(renormalize))
 
 
 class MoeError(RuntimeError):
@@ -97,6 +122,7 @@ def lib() -> ctypes.CDLL:
                           "`python -m sparse_moe_transformer_gemm_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    I32, L64 = ctypes.c_int32, ctypes.c_int64
     C = ctypes.POINTER(MoeConfig)
     sig = {
         "moe_workspace_size": (S, [C]),
@@ -120,6 +146,16 @@ def lib() -> ctypes.CDLL:
         "moe_forward3": (I, [C, P, P, P, P, P, P, P, P, P, P, S, P]),
         "moe_selftest_bounded_wait": (I, [P, ctypes.c_ulonglong, P]),
         "moe_ep_row_experts": (I, [P, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int32, P]),
+        "moe_select": (I, [C, P, L64, P, P, P, P, P]),
+        "moe_route4": (I, [C, P, P, P, P, P, P, P, P, S, P]),
+        "moe_forward4": (I, [C, P, P, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_forward_routed": (I, [C, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_block_quant": (I, [P, L64, I32, I32, P, P, P]),
+        "moe_block_gemm": (I, [P, P, P, P, P, I32, I32, I32, I32, P, I32, P, S, P]),
+        "moe_block_workspace_size": (S, [I32, I32, I32, I32]),
+        "moe_block_permute": (I, [C, P, P, P, P, P]),
+        "moe_block_gate_up": (I, [C, P, P, P, P, P, P, P, P, S, P]),
+        "moe_block_down": (I, [C, P, P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -131,14 +167,17 @@ def lib() -> ctypes.CDLL:
 
 def config(T: int, d: int, E: int, k: int, d_ff: int, scale: float = 2.826, fp8: bool = False,
            path: Optional[str] = None, packed: bool = False, shared: bool = False,
-           fp4: bool = False) -> MoeConfig:
+           fp4: bool = False, fp8_block: bool = False) -> MoeConfig:
     """Build a moe_config. path: None (automatic), "stream" or "gemm"; packed: the
     bf16 expert weights are in moe_pack_weights' layout; shared: expert E of the
     weight arrays is a shared expert; fp4: E2M1 expert weights with E8M0 block
-    scales."""
+    scales; fp8_block: e4m3 expert weights and activations with a scale per block of
+    128."""
     flags = MOE_FLAG_FP8_WEIGHTS if fp8 else 0
     if fp4:
         flags |= MOE_FLAG_FP4_WEIGHTS
+    if fp8_block:
+        flags |= MOE_FLAG_FP8_BLOCK
     if packed:
         flags |= MOE_FLAG_PACKED_WEIGHTS
     if shared:
@@ -305,6 +344,110 @@ def moe_ep_row_experts(counts, n_src: int, e_local: int, expert_of_row, stream=N
     _check("moe_ep_row_experts",
            lib().moe_ep_row_experts(_p(counts), int(n_src), int(e_local), _p(expert_of_row),
                                     int(expert_of_row.numel()), _s(stream)))
+
+
+def _opt(o):
+    return None if o is None else ctypes.byref(o)
+
+
+def _rows(fn: str, t: torch.Tensor, cols: int) -> int:
+    """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+
+
+def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
+    """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
+    if logits.dtype != torch.float32 or logits.shape[0] != cfg.T:
+        raise MoeError("moe_select", MOE_ERR_INVALID_ARG)
+    _check("moe_select", lib().moe_select(ctypes.byref(cfg), _p(logits),
+                                          _rows("moe_select", logits, cfg.E), _opt(opt),
+                                          _opt(grp), _p(topk_idx), _p(topk_w), _s(stream)))
+
+
+def moe_route4(cfg, x, w_gate, gate_bias, opt, grp, topk_idx, topk_w, ws, stream=None) -> None:
+    _check("moe_route4", lib().moe_route4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias),
+                                          _opt(opt), _opt(grp), _p(topk_idx), _p(topk_w), _p(ws),
+                                          ws.numel(), _s(stream)))
+
+
+def moe_forward4(cfg, x, w_gate, gate_bias, opt, grp, w_gate_up, s_gate_up, w_down, s_down, out,
+                 ws, stream=None) -> None:
+    _check("moe_forward4",
+           lib().moe_forward4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias), _opt(opt),
+                              _opt(grp), _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
+                              _p(out), _p(ws), ws.numel(), _s(stream)))
+
+
+def moe_forward_routed(cfg, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, out, ws,
+                       stream=None) -> None:
+    """The layer after its router, for a given routing."""
+    _check("moe_forward_routed",
+           lib().moe_forward_routed(ctypes.byref(cfg), _p(x), _p(topk_idx), _p(topk_w),
+                                    _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
+                                    _p(out), _p(ws), ws.numel(), _s(stream)))
+
+
+def moe_block_quant(x, codes, scales, stream=None) -> None:
+    """Quantise rows: x [M, K] bf16 (rows may be strided), codes [M, K] e4m3 (or uint8),
+    scales [M, ceil(K/128)] fp32."""
+    M, K = codes.shape
+    if x.dtype != torch.bfloat16 or x.shape != codes.shape or codes.element_size() != 1 or \
+            tuple(scales.shape) != (M, -(-K // 128)) or scales.dtype != torch.float32 or \
+            not codes.is_contiguous() or not scales.is_contiguous():
+        raise MoeError("moe_block_quant", MOE_ERR_INVALID_ARG)
+    _check("moe_block_quant",
+           lib().moe_block_quant(_p(x), _rows("moe_block_quant", x, K), M, K, _p(codes),
+                                 _p(scales), _s(stream)))
+
+
+def block_workspace(M: int, N: int, K: int, G: int = 1, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for moe_block_gemm calls of these sizes."""
+    n = int(lib().moe_block_workspace_size(G, M, N, K))
+    if n == 0:
+        raise MoeError("moe_block_workspace_size", MOE_ERR_UNSUPPORTED_SHAPE)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_block_gemm(xq, sx, wq, sw, out, ws, offsets=None, stream=None) -> None:
+    """out [M, N] (bf16 or fp32) = xq [M, K] times wq [N, K] transposed, e4m3 codes with a
+    scale per block of 128 (sx [M, ceil(K/128)], sw [ceil(N/128), ceil(K/128)]). With offsets
+    [G+1] int32, wq [G, N, K] and sw [G, ...]: rows [offsets[g], offsets[g+1]) take weight g."""
+    G = 1 if offsets is None else wq.shape[0]
+    N, K = wq.shape[-2:]
+    M = xq.shape[0]
+    kb, nb = -(-K // 128), -(-N // 128)
+    lead = () if offsets is None else (G,)
+    if tuple(xq.shape) != (M, K) or tuple(sx.shape) != (M, kb) or \
+            tuple(wq.shape) != lead + (N, K) or tuple(sw.shape) != lead + (nb, kb) or \
+            tuple(out.shape) != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
+            (offsets is not None and (offsets.numel() != G + 1 or offsets.dtype != torch.int32)) or \
+            xq.element_size() != 1 or wq.element_size() != 1 or sx.dtype != torch.float32 or \
+            sw.dtype != torch.float32 or not all(t.is_contiguous() for t in (xq, sx, wq, sw, out)):
+        raise MoeError("moe_block_gemm", MOE_ERR_INVALID_ARG)
+    _check("moe_block_gemm",
+           lib().moe_block_gemm(_p(xq), _p(sx), _p(wq), _p(sw), _p(offsets), G, M, N, K, _p(out),
+                                MOE_OUT_F32 if out.dtype == torch.float32 else MOE_OUT_BF16,
+                                _p(ws), ws.numel(), _s(stream)))
+
+
+def moe_block_permute(cfg, x, row_of, xq, sx, stream=None) -> None:
+    _check("moe_block_permute", lib().moe_block_permute(ctypes.byref(cfg), _p(x), _p(row_of),
+                                                        _p(xq), _p(sx), _s(stream)))
+
+
+def moe_block_gate_up(cfg, xq, sx, offsets, w_gate_up, s_gate_up, hq, sh, ws, stream=None) -> None:
+    _check("moe_block_gate_up",
+           lib().moe_block_gate_up(ctypes.byref(cfg), _p(xq), _p(sx), _p(offsets), _p(w_gate_up),
+                                   _p(s_gate_up), _p(hq), _p(sh), _p(ws), ws.numel(),
+                                   _s(stream)))
+
+
+def moe_block_down(cfg, hq, sh, offsets, w_down, s_down, y, ws, stream=None) -> None:
+    _check("moe_block_down",
+           lib().moe_block_down(ctypes.byref(cfg), _p(hq), _p(sh), _p(offsets), _p(w_down),
+                                _p(s_down), _p(y), _p(ws), ws.numel(), _s(stream)))
 
 
 def moe_read_status(ws, stream=None) -> int:
