@@ -75,6 +75,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     return mbar_wait_for(bar, parity, abort_flag, kWaitNs);
 }
 
+// The same for waits that a pipeline's step depends on: the wall clock is read
+// (which takes as long as several hand-offs) only after `POLLS` tries.
+template <int POLLS = 4096>
+__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
+                                              const volatile int* abort_flag) {
+    for (int i = 0; i < POLLS; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_for(bar, parity, abort_flag, kWaitNs);
+}
+
 // ------------------------------------------------------------------ TMA
 
 // 2-D tiled bulk tensor load into this CTA's shared memory, completion counted
@@ -186,6 +196,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// The same for an arrival that publishes no memory writes, only that this thread's
+// tensor-memory reads are complete (tmem_ld_wait): without the cluster-wide
+// release, whose fence takes about 2000 cycles.
+__device__ __forceinline__ void mbar_arrive_cluster_read(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) from
 // global memory into the shared memory of a CTA of the cluster, completing on an
 // mbarrier of that CTA (dst_cluster and bar_cluster from map_to_cta). Not
@@ -222,6 +239,17 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_pending() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Give up registers to, or take them from, the block's pool (all four warps of a
+// warpgroup; the shares have to add up to at most what the launch allocated).
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ------------------------------------------------------------------ tcgen05
@@ -323,6 +351,25 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         : "memory");
 }
 
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B (formats 0), fp32
+// accumulate, both operands K-major; the other fields as above.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The pair MMA on e4m3 operands, K = 32 (32 bytes of a row; the operand tiles
+// are rows of 128 bytes as desc_sw128 describes them).
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T across the pair: A is K-major in tensor
 // memory (row i of each CTA's 128 rows in its lane i, two bf16 per 32-bit
 // column, K = 16 in 8 columns), at the same column address in both CTAs.
@@ -386,6 +433,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
           "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
