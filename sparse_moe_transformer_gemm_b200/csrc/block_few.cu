@@ -1,0 +1,430 @@
+// block_few.cu -- block-scaled FP8 products for few rows a group (see
+// block_gemm.cu), on pairs of SMs (tcgen05 cta_group::2, kind::f8f6f4).
+//
+// The weight stream is the bound: every weight byte is read once and used for a
+// handful of tokens. The weight rows are the MMA's M (256 a pair and
+// accumulator, 128 a CTA) and up to 32 tokens its N, so a tile costs the tensor
+// core little; two accumulators share the staged tokens (gate_up: gate and up
+// rows, whose SiLU(g) u is then formed in registers; a plain product: two
+// 256-row tiles). A block's sums take 64 TMEM columns, so eight blocks are in
+// flight between the MMAs and the promotion, and the ring holds 6 x 32 KB of
+// weights per SM. (With two blocks in flight, which larger token tiles leave
+// room for, each block waited for the promotion's round trip: the Hy3 experts
+// at T = 64 took 740 us.)
+//
+// A thread of the promotion owns one weight row and 16 tokens of each
+// accumulator. A CTA's 128 weight rows of an accumulator lie in one block of
+// rows, so the factor sx[token] sw[rows] of a token is the same for the whole
+// CTA: a warp forms them in a ring in shared memory, ahead of the promotion.
+//
+// Per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM owner (+ MMA issuer in
+// the even CTA), warp 2 the factors, warps 4-11 promotion and epilogue in two
+// groups of four (one warp per TMEM lane quarter) with 16 tokens each. All
+// waits are bounded.
+#include "block_tile.cuh"
+
+namespace moe {
+namespace block {
+namespace {
+
+constexpr int BM = 128;                // weight rows per CTA and accumulator
+constexpr int A_BYTES = BM * BK;
+constexpr int NM = 32;                 // tokens per pair tile
+constexpr int CH = NM / 2;             // tokens per promotion group, and staged per CTA
+constexpr int STAGE_BYTES = 2 * A_BYTES + CH * BK;
+constexpr int STAGES = 6;
+constexpr int COLS = 2 * NM;           // TMEM columns per block
+constexpr int ACC = 512 / COLS;        // blocks in flight
+constexpr int SLOTS = 8;               // factor ring
+constexpr int SCALE_WARP = 2, PROMO_WARP = 4;
+constexpr int THREADS = 32 * (PROMO_WARP + 8);
+constexpr int EPI_BYTES = 2 * CH * BM * 2;  // a [16 tokens][128 rows] bf16 tile per group
+
+struct Ctrl {
+    uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
+    uint64_t empty[STAGES];   // both CTAs: the pair MMAs finished reading the stage
+    uint64_t acc_full[ACC];   // both CTAs: a block's sums are in TMEM
+    uint64_t acc_empty[ACC];  // even CTA: every promotion warp of both CTAs has read them
+    uint64_t sc_full[SLOTS];
+    uint64_t sc_empty[SLOTS];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    TileTable tab;
+    alignas(16) float scales[SLOTS][COLS];
+    alignas(16) uint32_t amax[2][CH][4];  // gate_up: a token's largest |h| per lane quarter
+    alignas(16) float4 hscale[2][CH];     // gate_up: BlockScale of a token
+};
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + (int)sizeof(Ctrl);
+static_assert(SMEM <= 232448, "fits in 227 KB");
+
+__device__ __forceinline__ void give_up(Ctrl& c, int* status) {
+    *reinterpret_cast<volatile int*>(&c.abort) = 1;
+    atomicExch(status, MOE_ERR_TIMEOUT);
+}
+
+// acc[token] += d[token] * s[token] (d: TMEM words, s: shared memory).
+__device__ __forceinline__ void promote(uint64_t (&acc)[CH / 2], const uint32_t (&d)[CH],
+                                        const float* s) {
+#pragma unroll
+    for (int i = 0; i < CH / 4; ++i) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s + 4 * i);
+        fma2(acc[2 * i], pack2(d[4 * i], d[4 * i + 1]), f.x);
+        fma2(acc[2 * i + 1], pack2(d[4 * i + 2], d[4 * i + 3]), f.y);
+    }
+}
+
+// tmA: weights [G * w_rows, K] bytes, box 128 x 128; tmB: tokens [M, K] bytes.
+template <bool GATE_UP, bool OUT_F32>
+__global__ void __launch_bounds__(THREADS, 1)
+block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
+                 const Args a) {
+    pdl_launch_and_wait();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* epi = smem + STAGES * STAGE_BYTES;
+    Ctrl& c = *reinterpret_cast<Ctrl*>(epi + EPI_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(tc::cluster_ctarank() & 1u);
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int KB = (a.K + BK - 1) / BK;
+
+    // ---- prologue: tile table (warp 0), barriers and TMEM (warp 1), in both CTAs
+    if (warp == 0) {
+        fill_table<NM>(c.tab, a);
+        if (lane == 0) {
+            c.abort = 0;
+            tc::prefetch_tensormap(&tmA);
+            tc::prefetch_tensormap(&tmB.m[0]);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int s = 0; s < STAGES; ++s) {
+                tc::mbar_init(&c.full[s], 1);
+                tc::mbar_init(&c.empty[s], 1);
+            }
+            for (int i = 0; i < ACC; ++i) {
+                tc::mbar_init(&c.acc_full[i], 1);
+                tc::mbar_init(&c.acc_empty[i], 2 * 8);
+            }
+            for (int i = 0; i < SLOTS; ++i) {
+                tc::mbar_init(&c.sc_full[i], 1);
+                tc::mbar_init(&c.sc_empty[i], 8);
+            }
+            tc::mbar_init(&c.drain, 1);
+            tc::fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc_pair(&c.tmem_base, 512);
+        tc::tmem_relinquish_pair();
+    }
+    tc::fence_before_sync();
+    tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+    tc::fence_after_sync();
+    const uint32_t tmem_base = c.tmem_base;
+    const int total = c.tab.total;
+    const volatile int* abort_flag = &c.abort;
+    // first weight row of a tile's accumulator p, within its group, for this CTA
+    auto first_row = [&](int m, int p) {
+        return GATE_UP ? p * a.N + m * 2 * BM + rank * BM : m * 4 * BM + p * 2 * BM + rank * BM;
+    };
+    // whether the pair's accumulator 1 has rows (always in gate_up)
+    auto two = [&](int m) { return GATE_UP || m * 4 * BM + 2 * BM < a.N; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- producer: this CTA's weight rows and 16 tokens
+            const uint64_t pol_w = tc::policy_evict_first();
+            const uint64_t pol_x = tc::policy_evict_last();
+            int stage = 0;
+            uint32_t phase = 0;
+            uint32_t parity[STAGES] = {};
+            bool issued[STAGES] = {};
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += n_pairs) {
+                const Tile ti = tile_of<NM>(c.tab, a.G, t);
+                const bool second = two(ti.m);
+                const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
+                const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
+                const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + CH * BK);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!tc::mbar_wait_hot(&c.empty[stage], phase ^ 1u, abort_flag)) {
+                        give_up(c, a.status);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
+                    uint8_t* s = smem + stage * STAGE_BYTES;
+                    if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
+                    tc::tma_load_2d_pair(s, &tmA, bar, kb * BK, w0, pol_w);
+                    if (second) tc::tma_load_2d_pair(s + A_BYTES, &tmA, bar, kb * BK, w1, pol_w);
+                    tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
+                                         ti.row0 + rank * CH, pol_x);
+                    issued[stage] = true;
+                    parity[stage] = phase;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // drain: this CTA's copies have landed (the even CTA's full barrier saw
+            // every byte of both CTAs when its last phase completed)
+            const int zero = 0;
+            for (int s = 0; s < STAGES; ++s)
+                if (issued[s] && !tc::mbar_wait(leader ? &c.full[s] : &c.empty[s], parity[s], &zero))
+                    atomicExch(a.status, MOE_ERR_TIMEOUT);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- MMA issuer (even CTA): 256 weight rows x 32 tokens, twice
+            const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, NM);
+            int stage = 0;
+            uint32_t phase = 0, blk = 0;
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += n_pairs) {
+                const bool second = two(tile_of<NM>(c.tab, a.G, t).m);
+                for (int kb = 0; kb < KB; ++kb, ++blk) {
+                    const uint32_t as = blk % ACC;
+                    if (!tc::mbar_wait_hot(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
+                        !tc::mbar_wait_hot(&c.full[stage], phase, abort_flag)) {
+                        give_up(c, a.status);
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t d = tmem_base + as * COLS;
+                    const uint32_t w = tc::smem_u32(smem + stage * STAGE_BYTES);
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k) {
+                        const uint64_t x = tc::desc_sw128(w + 2 * A_BYTES + k * 32);
+                        tc::mma_e4m3_pair(d, tc::desc_sw128(w + k * 32), x, idesc, k > 0);
+                        if (second)
+                            tc::mma_e4m3_pair(d + NM, tc::desc_sw128(w + A_BYTES + k * 32), x,
+                                              idesc, k > 0);
+                    }
+                    tc::mma_commit_pair(&c.empty[stage], 0x3);
+                    tc::mma_commit_pair(&c.acc_full[as], 0x3);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            tc::mma_commit_pair(&c.drain, 0x1);
+            const int zero = 0;
+            if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
+        }
+    } else if (warp == SCALE_WARP) {
+        // ---------------- factors: per block sx[token] * sw of this CTA's weight rows,
+        // lane = token, 4 blocks loaded at a time. The ring runs ahead of the
+        // promotion, over tile borders too.
+        constexpr int U = 4;
+        const int nb_n = (a.N + 127) / 128;
+        const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
+        uint32_t blk = 0;
+        bool ok = true;
+        for (int t = pair; t < total && ok; t += n_pairs) {
+            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            const float* sxp = a.sx + (size_t)(ti.row0 + lane) * KB;
+            const float* swp[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int nb = min(first_row(ti.m, p) / BM, sw_rows - 1);
+                swp[p] = a.sw + ((size_t)ti.g * sw_rows + nb) * KB;
+            }
+            for (int k0 = 0; k0 < KB && ok; k0 += U) {
+                float x[U], w[2][U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool in = k0 + u < KB;
+                    w[0][u] = in ? swp[0][k0 + u] : 0.f;
+                    w[1][u] = in ? swp[1][k0 + u] : 0.f;
+                    x[u] = in && lane < ti.len ? sxp[k0 + u] : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (k0 + u >= KB || !ok) continue;
+                    const uint32_t slot = blk % SLOTS;
+                    ok = tc::mbar_wait_hot(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u, abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) {
+                        give_up(c, a.status);
+                        continue;
+                    }
+                    c.scales[slot][lane] = x[u] * w[0][u];
+                    c.scales[slot][NM + lane] = x[u] * w[1][u];
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
+                    ++blk;
+                }
+            }
+        }
+    } else if (warp >= PROMO_WARP) {
+        // ---------------- promotion and epilogue: lane = one weight row of each
+        // accumulator; group grp takes the tokens [16 grp, 16 grp + 16)
+        const int quad = warp & 3, grp = (warp - PROMO_WARP) >> 2;
+        const int et = threadIdx.x - 32 * PROMO_WARP - 128 * grp;  // 0..127 within the group
+        const int bar = 1 + grp;
+        const int row = quad * 32 + lane;                          // of the CTA's 128
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16) + grp * CH;
+        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0]), 0);
+        uint8_t* tile = epi + grp * (EPI_BYTES / 2);
+        uint32_t blk = 0;
+        for (int t = pair; t < total; t += n_pairs) {
+            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            const int left = ti.len - grp * CH;  // valid tokens of this group
+            const long tok0 = ti.row0 + grp * CH;
+            const bool second = two(ti.m);
+            uint64_t acc[2][CH / 2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int j = 0; j < CH / 2; ++j) acc[p][j] = 0;
+            bool ok = true;
+            for (int kb = 0; kb < KB; ++kb, ++blk) {
+                const uint32_t as = blk % ACC, slot = blk % SLOTS;
+                ok = tc::mbar_wait_hot(&c.sc_full[slot], (blk / SLOTS) & 1u, abort_flag) &&
+                     tc::mbar_wait_hot(&c.acc_full[as], (blk / ACC) & 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);  // the warp stays together
+                if (!ok) break;
+                if (left > 0) {
+                    tc::fence_after_sync();
+                    const uint32_t tb = lane_base + as * COLS;
+                    uint32_t d0[CH], d1[CH];
+                    tc::tmem_ld16(tb, d0);
+                    if (second) tc::tmem_ld16(tb + NM, d1);
+                    tc::tmem_ld_wait();
+                    tc::tmem_loaded(d0);
+                    if (second) tc::tmem_loaded(d1);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
+                    promote(acc[0], d0, c.scales[slot] + grp * CH);
+                    if (second) promote(acc[1], d1, c.scales[slot] + NM + grp * CH);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&c.sc_empty[slot]);
+                } else if (lane == 0) {
+                    tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
+                    tc::mbar_arrive(&c.sc_empty[slot]);
+                }
+            }
+            // a warp that gave up takes its group with it
+            if (tc::bar_any(bar, 128, !ok)) {
+                give_up(c, a.status);
+                break;
+            }
+            if (left <= 0) continue;
+            if constexpr (GATE_UP) {
+                const int f0 = ti.m * 2 * BM + rank * BM;  // first feature of the CTA's block
+                uint32_t mx = 0;
+#pragma unroll
+                for (int j = 0; j < CH; j += 2) {
+                    const float h0 = silu_mul(value_at(acc[0], j), value_at(acc[1], j));
+                    const float h1 = silu_mul(value_at(acc[0], j + 1), value_at(acc[1], j + 1));
+                    acc[0][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
+                    const uint32_t m0 = __reduce_max_sync(0xffffffffu, f32_bits(h0) & 0x7FFFFFFFu);
+                    const uint32_t m1 = __reduce_max_sync(0xffffffffu, f32_bits(h1) & 0x7FFFFFFFu);
+                    if (lane == j) mx = m0;
+                    if (lane == j + 1) mx = m1;
+                }
+                if (lane < CH) c.amax[grp][lane][quad] = mx;
+                tc::bar_sync(bar, 128);
+                if (et < CH) {
+                    const uint4 m = *reinterpret_cast<const uint4*>(c.amax[grp][et]);
+                    const BlockScale b =
+                        block_scale(f32_from_bits(max(max(m.x, m.y), max(m.z, m.w))));
+                    c.hscale[grp][et] = make_float4(b.a, b.inv, b.move, b.scale);
+                    if (et < left && f0 < a.N)
+                        a.out_scales[(tok0 + et) * (a.N / 128) + (f0 >> 7)] = b.scale;
+                }
+                tc::bar_sync(bar, 128);
+                // codes through a [16 tokens][128 features] tile to 16-byte stores
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    const float4 v = c.hscale[grp][j];
+                    const BlockScale b = {v.w, v.x, v.y, v.z};
+                    tile[j * BM + row] =
+                        (uint8_t)e4m3x2_of(block_quotient(b, value_at(acc[0], j)), 0.f);
+                }
+                tc::bar_sync(bar, 128);
+                const int n = et / (BM / 16), ch = et % (BM / 16);
+                if (f0 < a.N && n < left)
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (tok0 + n) * a.N + f0 +
+                                              ch * 16) =
+                        *reinterpret_cast<const uint4*>(tile + n * BM + ch * 16);
+                // (the next tile's bar_any comes before the next writes here)
+            } else {
+                const bool vec = !OUT_F32 && a.N % 8 == 0;
+                uint16_t* o = reinterpret_cast<uint16_t*>(tile);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int n0 = first_row(ti.m, p);  // first output column
+                    if (p == 1 && !second) continue;
+                    if (vec) {
+                        // through a [16 tokens][128 rows] tile to 16-byte stores
+                        if (p == 1) tc::bar_sync(bar, 128);  // the first half is read
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            o[j * BM + row] = float_to_bf16_bits(value_at(acc[p], j));
+                        tc::bar_sync(bar, 128);
+#pragma unroll
+                        for (int q = 0; q < CH * BM / 8 / 128; ++q) {
+                            const int id = et + 128 * q;
+                            const int n = id / (BM / 8), ch = id % (BM / 8);
+                            if (n < left && n0 + ch * 8 < a.N)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                          (tok0 + n) * a.N + n0 + ch * 8) =
+                                    *reinterpret_cast<const uint4*>(o + n * BM + ch * 8);
+                        }
+                    } else if (n0 + row < a.N) {
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            if (j < left) {
+                                const long at = (tok0 + j) * a.N + n0 + row;
+                                if (OUT_F32)
+                                    static_cast<float*>(a.out)[at] = value_at(acc[p], j);
+                                else
+                                    static_cast<uint16_t*>(a.out)[at] =
+                                        float_to_bf16_bits(value_at(acc[p], j));
+                            }
+                    }
+                }
+            }
+        }
+    }
+
+    // Neither CTA leaves while the other may still signal its barriers or read
+    // its shared memory.
+    tc::fence_before_sync();
+    tc::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc::fence_after_sync();
+        tc::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
+    const int w_rows = gate_up ? 2 * p.N : p.N;
+    const int per_tile = gate_up ? 2 * BM : 4 * BM;
+    const Args a = {p.sx, p.sw, p.offsets, p.G, p.M, p.N, p.K, (p.N + per_tile - 1) / per_tile,
+                    w_rows, p.out, p.out_scales, p.status};
+    CUtensorMap ma;
+    TokenMaps mb;
+    if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K))
+        return cudaErrorInvalidValue;
+    if (gate_up)
+        return launch_pairs(block_few_kernel<true, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+    if (p.out_type == MOE_OUT_F32)
+        return launch_pairs(block_few_kernel<false, true>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+    return launch_pairs(block_few_kernel<false, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+}
+
+}  // namespace block
+}  // namespace moe

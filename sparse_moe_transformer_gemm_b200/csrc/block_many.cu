@@ -1,0 +1,446 @@
+// block_many.cu -- block-scaled FP8 products for many rows a group (see
+// block_gemm.cu), on pairs of SMs (tcgen05 cta_group::2, kind::f8f6f4).
+//
+// A pair tile is 256 tokens (the MMA's M, 128 a CTA) times 256 weight rows (its N,
+// each CTA staging 128 of them): 32 KB through shared memory per CTA and block
+// of 128 columns, four K = 32 MMAs into one of two 256-column TMEM accumulators
+// that start from zero. A thread of the promotion owns one token and 128 of the
+// tile's columns: the block's factor sx[token] sw[rows] is one register for all
+// of them (two in gate_up), and the sum of a block is one tcgen05.ld and one
+// fused multiply-add per value. (With the weight rows in M and the tokens in N
+// the factors differ per column and come from shared memory, 16 bytes per 4
+// values and thread: the product 8192 x 8192 x 4096 took 706 us that way.)
+//
+// gate_up: columns 0-127 are the gate rows of one 128-feature block (staged by
+// the even CTA), 128-255 its up rows (the odd CTA). A thread holds 64 gate and
+// the same 64 up values of its token, so SiLU(g) u, the token's largest |h| and
+// the codes need no exchange but one float between its two threads.
+//
+// Per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM owner (+ MMA issuer in
+// the even CTA), warp 2 the factors (a ring in shared memory), warps 4-11 promotion and epilogue, in two groups of four (one
+// warp per 32 TMEM lanes) with half of the columns each. The promotion's threads
+// hold 128 accumulators, so the first four warps hand registers over
+// (setmaxnreg). All waits are bounded.
+#include "block_tile.cuh"
+
+namespace moe {
+namespace block {
+namespace {
+
+constexpr int BM = 128;                // tokens, and weight rows, a CTA stages
+constexpr int NM = 2 * BM;             // tokens per pair tile
+constexpr int STAGE_BYTES = 2 * BM * BK;
+constexpr int STAGES = 6;
+constexpr int COLS = 256;              // TMEM columns per block
+constexpr int PROMO_WARP = 4;          // the first of 8
+constexpr int THREADS = 32 * (PROMO_WARP + 8);
+constexpr int CH = 64;                 // columns per tcgen05.ld
+constexpr int SCALE_WARP = 2;
+constexpr int SLOTS = 8;               // factor ring
+constexpr int EPI_COLS = 32;           // columns per pass of the store staging
+constexpr int EPI_BYTES = 8 * 32 * EPI_COLS * 2;  // [32 tokens][32 columns] bf16 per warp
+// registers a thread: 168 at launch; 3 * 168 = 72 + 2 * 216
+constexpr int REGS_FEW = 72, REGS_MANY = 216;
+static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
+
+struct Ctrl {
+    uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
+    uint64_t empty[STAGES];   // both CTAs: the pair MMAs finished reading the stage
+    uint64_t acc_full[2];     // both CTAs: a block's sums are in TMEM
+    uint64_t acc_empty[2];    // even CTA: every promotion warp of both CTAs has read them
+    uint64_t sc_full[SLOTS];
+    uint64_t sc_empty[SLOTS];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    TileTable tab;
+    float amax[2][BM];        // gate_up: a token's largest |h| in each group's columns
+    float factor[SLOTS][2][BM];  // sx[token] * sw of the columns 0-127 and 128-255
+};
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + (int)sizeof(Ctrl);
+static_assert(SMEM <= 232448, "fits in 227 KB");
+
+__device__ __forceinline__ void give_up(Ctrl& c, int* status) {
+    *reinterpret_cast<volatile int*>(&c.abort) = 1;
+    atomicExch(status, MOE_ERR_TIMEOUT);
+}
+
+__device__ __forceinline__ void promote(uint64_t (&acc)[CH / 2], const uint32_t (&d)[CH], float f) {
+    const uint64_t ff = pack2(f32_bits(f), f32_bits(f));
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) fma2(acc[i], pack2(d[2 * i], d[2 * i + 1]), ff);
+}
+
+// tmA: weights [G * w_rows, K] bytes, box 128 x 128; tmB: tokens [M, K] bytes.
+template <bool GATE_UP, bool OUT_F32>
+__global__ void __launch_bounds__(THREADS, 1)
+block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
+                  const Args a) {
+    pdl_launch_and_wait();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* epi = smem + STAGES * STAGE_BYTES;
+    Ctrl& c = *reinterpret_cast<Ctrl*>(epi + EPI_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(tc::cluster_ctarank() & 1u);
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int KB = (a.K + BK - 1) / BK;
+
+    // ---- prologue: tile table (warp 0), barriers and TMEM (warp 1), in both CTAs
+    if (warp == 0) {
+        fill_table<NM>(c.tab, a);
+        if (lane == 0) {
+            c.abort = 0;
+            tc::prefetch_tensormap(&tmA);
+            for (int m = 0; m < 4; ++m) tc::prefetch_tensormap(&tmB.m[m]);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int s = 0; s < STAGES; ++s) {
+                tc::mbar_init(&c.full[s], 1);
+                tc::mbar_init(&c.empty[s], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(&c.acc_full[i], 1);
+                tc::mbar_init(&c.acc_empty[i], 2 * 8);
+            }
+            for (int i = 0; i < SLOTS; ++i) {
+                tc::mbar_init(&c.sc_full[i], 1);
+                tc::mbar_init(&c.sc_empty[i], 8);
+            }
+            tc::mbar_init(&c.drain, 1);
+            tc::fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc_pair(&c.tmem_base, 512);
+        tc::tmem_relinquish_pair();
+    }
+    tc::fence_before_sync();
+    tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+    tc::fence_after_sync();
+    const uint32_t tmem_base = c.tmem_base;
+    const int total = c.tab.total;
+    const volatile int* abort_flag = &c.abort;
+
+    if (warp >= PROMO_WARP) {
+        tc::regs_inc<REGS_MANY>();
+        // ---------------- promotion and epilogue: lane = one token of this CTA's
+        const int quad = warp & 3, grp = (warp - PROMO_WARP) >> 2;
+        const int row = quad * 32 + lane;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
+        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0]), 0);
+        // the two chunks of this thread's columns: gate_up 64 gate columns and their
+        // up ones
+        const int col0 = GATE_UP ? grp * CH : grp * 2 * CH;
+        const int col1 = GATE_UP ? 2 * CH + grp * CH : grp * 2 * CH + CH;
+        const int nb_n = (a.N + 127) / 128;
+        uint32_t blk = 0;
+        for (int t = pair; t < total; t += n_pairs) {
+            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            const int tok = rank * BM + row;                     // token within the tile
+            const bool mine = tok < ti.len;
+            const bool active = rank * BM + quad * 32 < ti.len;  // any token of the warp
+            uint64_t acc[2][CH / 2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < CH / 2; ++j) acc[i][j] = 0;
+            bool ok = true;
+            for (int kb = 0; kb < KB; ++kb, ++blk) {
+                const uint32_t as = blk & 1u, slot = blk % SLOTS;
+                ok = tc::mbar_wait_hot(&c.sc_full[slot], (blk / SLOTS) & 1u, abort_flag) &&
+                     tc::mbar_wait_hot(&c.acc_full[as], (blk >> 1) & 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);  // the warp stays together
+                if (!ok) break;
+                if (active) {
+                    tc::fence_after_sync();
+                    const uint32_t tb = lane_base + as * COLS;
+                    uint32_t d[CH];
+                    tc::tmem_ld64(tb + col0, d);
+                    const float f0 = c.factor[slot][GATE_UP ? 0 : grp][row];
+                    const float f1 = GATE_UP ? c.factor[slot][1][row] : f0;
+                    tc::tmem_ld_wait();
+                    tc::tmem_loaded(d);
+                    promote(acc[0], d, f0);
+                    tc::tmem_ld64(tb + col1, d);
+                    tc::tmem_ld_wait();
+                    tc::tmem_loaded(d);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
+                        tc::mbar_arrive(&c.sc_empty[slot]);
+                    }
+                    promote(acc[1], d, f1);
+                } else if (lane == 0) {
+                    tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
+                    tc::mbar_arrive(&c.sc_empty[slot]);
+                }
+            }
+            if constexpr (GATE_UP) {
+                // h in acc[0]; the token's largest |h| over both groups' columns
+                uint32_t mx = 0;
+#pragma unroll
+                for (int j = 0; j < CH; j += 2) {
+                    const float h0 = silu_mul(value_at(acc[0], j), value_at(acc[1], j));
+                    const float h1 = silu_mul(value_at(acc[0], j + 1), value_at(acc[1], j + 1));
+                    acc[0][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
+                    mx = max(mx, max(f32_bits(h0) & 0x7FFFFFFFu, f32_bits(h1) & 0x7FFFFFFFu));
+                }
+                c.amax[grp][row] = f32_from_bits(mx);
+                // (a warp that gave up takes the others with it)
+                if (tc::bar_any(1, 256, !ok)) {
+                    give_up(c, a.status);
+                    break;
+                }
+                const BlockScale b =
+                    block_scale(f32_from_bits(max(mx, f32_bits(c.amax[grp ^ 1][row]))));
+                if (mine) {
+                    const long r = ti.row0 + tok;
+                    if (grp == 0) a.out_scales[r * nb_n + ti.m] = b.scale;
+                    uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + r * a.N +
+                                                        ti.m * 128 + grp * 64);
+#pragma unroll
+                    for (int q = 0; q < CH / 16; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const int j = q * 16 + v * 4;
+                            w[v] = e4m3x2_of(block_quotient(b, value_at(acc[0], j)),
+                                             block_quotient(b, value_at(acc[0], j + 1))) |
+                                   (e4m3x2_of(block_quotient(b, value_at(acc[0], j + 2)),
+                                              block_quotient(b, value_at(acc[0], j + 3)))
+                                    << 16);
+                        }
+                        o[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                tc::bar_sync(1, 256);  // amax is read before the next tile's
+            } else {
+                if (!ok) {
+                    give_up(c, a.status);
+                    break;
+                }
+                if (!active) continue;
+                const int n0 = ti.m * COLS + grp * 128;          // first output column
+                const int rows = ti.len - rank * BM - quad * 32; // tokens of this warp
+                const long r0 = ti.row0 + rank * BM + quad * 32;
+                if (!OUT_F32 && a.N % 8 == 0) {
+                    // 32 columns at a time through the warp's [32 tokens][32 columns]
+                    // tile, 16-byte pieces swizzled by the token: 64-byte row segments
+                    // go out four lanes a row
+                    uint4* st = reinterpret_cast<uint4*>(
+                        epi + (warp - PROMO_WARP) * (EPI_BYTES / 8));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        __syncwarp();  // the previous pass is read
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const auto& v = acc[i >> 1];
+                            const int j = (i & 1) * 32 + q * 8;
+                            st[lane * 4 + (q ^ ((lane >> 1) & 3))] = make_uint4(
+                                pack_bf16x2(value_at(v, j), value_at(v, j + 1)),
+                                pack_bf16x2(value_at(v, j + 2), value_at(v, j + 3)),
+                                pack_bf16x2(value_at(v, j + 4), value_at(v, j + 5)),
+                                pack_bf16x2(value_at(v, j + 6), value_at(v, j + 7)));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int n = q * 8 + (lane >> 2), ch = lane & 3;
+                            const int col = n0 + i * 32 + ch * 8;
+                            if (n < rows && col < a.N)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                          (r0 + n) * a.N + col) =
+                                    st[n * 4 + (ch ^ ((n >> 1) & 3))];
+                        }
+                    }
+                } else if (mine) {
+                    const size_t at = (size_t)(ti.row0 + tok) * a.N + n0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            if (n0 + i * CH + j < a.N) {
+                                if (OUT_F32)
+                                    static_cast<float*>(a.out)[at + i * CH + j] =
+                                        value_at(acc[i], j);
+                                else
+                                    static_cast<uint16_t*>(a.out)[at + i * CH + j] =
+                                        float_to_bf16_bits(value_at(acc[i], j));
+                            }
+                }
+            }
+        }
+    } else {
+        tc::regs_dec<REGS_FEW>();
+        if (warp == 0) {
+            if (lane == 0) {
+                // ---------------- producer: this CTA's 128 tokens and 128 weight rows
+                const uint64_t pol_w = tc::policy_evict_first();
+                const uint64_t pol_x = tc::policy_evict_last();
+                int stage = 0;
+                uint32_t phase = 0;
+                uint32_t parity[STAGES] = {};
+                bool issued[STAGES] = {};
+                bool ok = true;
+                for (int t = pair; t < total && ok; t += n_pairs) {
+                    const Tile ti = tile_of<NM>(c.tab, a.G, t);
+                    // the rows that exist, in 16-row boxes (what the rest of the stage
+                    // holds only reaches TMEM lanes that nobody reads)
+                    const int r0 = (min(ti.len, BM) + 15) & ~15;
+                    const int r1 = (max(ti.len - BM, 0) + 15) & ~15;
+                    const int rows = leader ? r0 : r1;
+                    const int w0 = ti.g * a.w_rows +
+                                   (GATE_UP ? ti.m * BM + rank * a.N : ti.m * COLS + rank * BM);
+                    const uint32_t bytes = (uint32_t)(2 * BM + r0 + r1) * BK;
+                    for (int kb = 0; kb < KB; ++kb) {
+                        if (!tc::mbar_wait_hot(&c.empty[stage], phase ^ 1u, abort_flag)) {
+                            give_up(c, a.status);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
+                        uint8_t* s = smem + stage * STAGE_BYTES;
+                        if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
+                        tc::tma_load_2d_pair(s + BM * BK, &tmA, bar, kb * BK, w0, pol_w);
+                        load_tokens(s, tmB, bar, kb * BK, ti.row0 + rank * BM, rows, pol_x);
+                        issued[stage] = true;
+                        parity[stage] = phase;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                // drain: this CTA's copies have landed (the even CTA's full barrier saw
+                // every byte of both CTAs when its last phase completed)
+                const int zero = 0;
+                for (int s = 0; s < STAGES; ++s)
+                    if (issued[s] &&
+                        !tc::mbar_wait(leader ? &c.full[s] : &c.empty[s], parity[s], &zero))
+                        atomicExch(a.status, MOE_ERR_TIMEOUT);
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && leader) {
+                // ---------------- MMA issuer (even CTA): 256 tokens x 256 weight rows
+                const uint32_t idesc = tc::idesc_e4m3_f32(NM, COLS);
+                int stage = 0;
+                uint32_t phase = 0, blk = 0;
+                bool ok = true;
+                for (int t = pair; t < total && ok; t += n_pairs) {
+                    for (int kb = 0; kb < KB; ++kb, ++blk) {
+                        const uint32_t as = blk & 1u;
+                        if (!tc::mbar_wait_hot(&c.acc_empty[as], ((blk >> 1) & 1u) ^ 1u,
+                                               abort_flag) ||
+                            !tc::mbar_wait_hot(&c.full[stage], phase, abort_flag)) {
+                            give_up(c, a.status);
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t x = tc::smem_u32(smem + stage * STAGE_BYTES);
+#pragma unroll
+                        for (int k = 0; k < BK / 32; ++k)
+                            tc::mma_e4m3_pair(tmem_base + as * COLS, tc::desc_sw128(x + k * 32),
+                                              tc::desc_sw128(x + BM * BK + k * 32), idesc, k > 0);
+                        tc::mma_commit_pair(&c.empty[stage], 0x3);
+                        tc::mma_commit_pair(&c.acc_full[as], 0x3);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                tc::mma_commit_pair(&c.drain, 0x1);
+                const int zero = 0;
+                if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
+            }
+        } else if (warp == SCALE_WARP) {
+            // ---------------- factors: per block sx[token] * sw of each half of the
+            // columns, 4 tokens a lane, U blocks loaded at a time; the ring runs ahead
+            // of the promotion, over tile borders too
+            constexpr int U = 4;
+            const int nb_n = (a.N + 127) / 128;
+            const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
+            uint32_t blk = 0;
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += n_pairs) {
+                const Tile ti = tile_of<NM>(c.tab, a.G, t);
+                const float* sxp = a.sx + (size_t)(ti.row0 + rank * BM + lane) * KB;
+                const int left = ti.len - rank * BM - lane;
+                const int nb0 = GATE_UP ? ti.m : ti.m * 2;
+                const int nb1 = GATE_UP ? nb_n + ti.m : min(ti.m * 2 + 1, nb_n - 1);
+                const float* sw0 = a.sw + ((size_t)ti.g * sw_rows + nb0) * KB;
+                const float* sw1 = a.sw + ((size_t)ti.g * sw_rows + nb1) * KB;
+                for (int k0 = 0; k0 < KB && ok; k0 += U) {
+                    float x[4][U], w0[U], w1[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool in = k0 + u < KB;
+                        w0[u] = in ? sw0[k0 + u] : 0.f;
+                        w1[u] = in ? sw1[k0 + u] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i][u] = in && 32 * i < left ? sxp[(size_t)(32 * i) * KB + k0 + u]
+                                                          : 0.f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (k0 + u >= KB || !ok) continue;
+                        const uint32_t slot = blk % SLOTS;
+                        ok = tc::mbar_wait_hot(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u,
+                                               abort_flag);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) {
+                            give_up(c, a.status);
+                            continue;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            c.factor[slot][0][lane + 32 * i] = x[i][u] * w0[u];
+                            c.factor[slot][1][lane + 32 * i] = x[i][u] * w1[u];
+                        }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
+                        ++blk;
+                    }
+                }
+            }
+        }
+    }
+
+    // Neither CTA leaves while the other may still signal its barriers or read
+    // its shared memory.
+    tc::fence_before_sync();
+    tc::cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc::fence_after_sync();
+        tc::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s) {
+    const int w_rows = gate_up ? 2 * p.N : p.N;
+    const int per_tile = gate_up ? BM : COLS;
+    const Args a = {p.sx, p.sw, p.offsets, p.G, p.M, p.N, p.K, (p.N + per_tile - 1) / per_tile,
+                    w_rows, p.out, p.out_scales, p.status};
+    CUtensorMap ma;
+    TokenMaps mb;
+    if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K))
+        return cudaErrorInvalidValue;
+    if (gate_up)
+        return launch_pairs(block_many_kernel<true, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+    if (p.out_type == MOE_OUT_F32)
+        return launch_pairs(block_many_kernel<false, true>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+    return launch_pairs(block_many_kernel<false, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+}
+
+}  // namespace block
+}  // namespace moe

@@ -1,0 +1,157 @@
+// block_tile.cuh -- what the two block-FP8 product kernels share: the arguments,
+// the table of tiles and the tensor maps.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "internal.h"
+#include "quant.cuh"
+#include "tc.cuh"
+
+namespace moe {
+namespace block {
+
+constexpr int BK = 128;       // columns per scale block = bytes per staged row
+constexpr int MAX_G = 257;    // 256 experts and a shared one
+constexpr int NBOX = 16;      // rows of the smallest token box
+
+struct Args {
+    const float* sx;
+    const float* sw;
+    const int* offsets;
+    int G, M, N, K;    // N: output features (gate_up: d_ff)
+    int m_tiles;       // weight tiles of a group
+    int w_rows;        // weight rows of a group (gate_up: 2 * d_ff)
+    void* out;
+    float* out_scales;
+    int* status;
+};
+
+// Token rows [M, K] bytes, boxes of 16, 32, 64 and 128 rows x 128 bytes.
+struct TokenMaps {
+    CUtensorMap m[4];
+};
+
+struct TileTable {
+    int total;
+    int off[MAX_G + 1];         // rows of group g: [off[g], off[g + 1])
+    int tile_start[MAX_G + 1];  // its first tile
+};
+
+struct Tile {
+    int g, m, row0, len;
+};
+
+// One warp fills the table: ceil(rows / NM) token tiles per weight tile. Offsets
+// are clamped to [0, M], so that no bad value leads outside the buffers.
+template <int NM>
+__device__ __forceinline__ void fill_table(TileTable& c, const Args& a) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int b = 0; b <= a.G; b += 32) {
+        const int g = b + lane;
+        auto offset = [&](int i) {
+            if (!a.offsets) return i == 0 ? 0 : a.M;
+            return min(max(a.offsets[i], 0), a.M);
+        };
+        int cnt = 0;
+        if (g <= a.G) {
+            const int o = offset(g);
+            c.off[g] = o;
+            if (g < a.G) cnt = max(0, (offset(g + 1) - o + NM - 1) / NM) * a.m_tiles;
+        }
+        int incl = cnt;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, s);
+            if (lane >= s) incl += v;
+        }
+        if (g < a.G) c.tile_start[g] = carry + incl - cnt;
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+        c.tile_start[a.G] = carry;
+        c.total = carry;
+    }
+}
+
+// Tile t: token tiles fastest (tiles that read the same weights are neighbours in
+// time, so HBM gives them once and L2 the other times), then weight tiles, then
+// groups.
+template <int NM>
+__device__ __forceinline__ Tile tile_of(const TileTable& c, int G, int t) {
+    int lo = 0, hi = G - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (c.tile_start[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int rows = c.off[lo + 1] - c.off[lo];
+    const int nt = (rows + NM - 1) / NM;
+    const int local = t - c.tile_start[lo];
+    const int m = local / nt, j = local - m * nt;
+    return Tile{lo, m, c.off[lo] + j * NM, min(NM, rows - j * NM)};
+}
+
+// `rows` (a multiple of 16, at most 128) token rows from `row` on, as at most
+// four boxes, completing on the even CTA's barrier.
+__device__ __forceinline__ void load_tokens(uint8_t* dst, const TokenMaps& tm, uint32_t bar,
+                                            int col, int row, int rows, uint64_t policy) {
+    for (int o = 0; o < rows;) {
+        const int rem = rows - o;
+        const int lg = rem >= 128 ? 3 : rem >= 64 ? 2 : rem >= 32 ? 1 : 0;
+        tc::tma_load_2d_pair(dst + o * BK, &tm.m[lg], bar, col, row + o, policy);
+        o += NBOX << lg;
+    }
+}
+
+// a += d * s on two fp32 values at a time.
+__device__ __forceinline__ void fma2(uint64_t& a, uint64_t d, uint64_t s) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ float value_at(const uint64_t (&a)[N], int i) {
+    return __uint_as_float((uint32_t)(a[i >> 1] >> (32 * (i & 1))));
+}
+
+// Host: maps and launch. make_byte_map: row-major [rows, cols] bytes, box of
+// box_rows rows x 128 bytes, 128-byte swizzle.
+bool make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                   uint32_t box_rows);
+bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64_t cols);
+int sm_pairs();
+
+template <typename Kernel>
+cudaError_t launch_pairs(Kernel kernel, int pairs, int threads, int smem, cudaStream_t s,
+                         const CUtensorMap& ma, const TokenMaps& mb, const Args& a) {
+    cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// The two kernels' launchers (block_few.cu, block_many.cu).
+cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s);
+cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s);
+
+}  // namespace block
+}  // namespace moe
