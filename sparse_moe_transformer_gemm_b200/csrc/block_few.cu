@@ -81,11 +81,10 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                  const Args a) {
     pdl_launch_and_wait();
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // stays a shared pointer
     uint8_t* epi = smem + STAGES * STAGE_BYTES;
     Ctrl& c = *reinterpret_cast<Ctrl*>(epi + EPI_BYTES);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)(tc::cluster_ctarank() & 1u);
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
@@ -123,8 +122,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc::fence_before_sync();
     tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc::fence_after_sync();
-    const uint32_t tmem_base = c.tmem_base;
-    const int total = c.tab.total;
+    const uint32_t tmem_base = tc::uniform(c.tmem_base);
+    const int total = (int)tc::uniform(c.tab.total);
     const volatile int* abort_flag = &c.abort;
     // first weight row of a tile's accumulator p, within its group, for this CTA
     auto first_row = [&](int m, int p) {
@@ -134,62 +133,56 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     auto two = [&](int m) { return GATE_UP || m * 4 * BM + 2 * BM < a.N; };
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- producer: this CTA's weight rows and 16 tokens
-            const uint64_t pol_w = tc::policy_evict_first();
-            const uint64_t pol_x = tc::policy_evict_last();
-            int stage = 0;
-            uint32_t phase = 0;
-            uint32_t parity[STAGES] = {};
-            bool issued[STAGES] = {};
-            bool ok = true;
-            for (int t = pair; t < total && ok; t += n_pairs) {
-                const Tile ti = tile_of<NM>(c.tab, a.G, t);
-                const bool second = two(ti.m);
-                const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
-                const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
-                const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + CH * BK);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!tc::mbar_wait_hot(&c.empty[stage], phase ^ 1u, abort_flag)) {
-                        give_up(c, a.status);
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
-                    uint8_t* s = smem + stage * STAGE_BYTES;
+        // ---------------- producer: this CTA's weight rows and 16 tokens
+        const uint64_t pol_w = tc::policy_evict_first();
+        const uint64_t pol_x = tc::policy_evict_last();
+        uint32_t it = 0;  // blocks loaded
+        bool ok = true;
+        for (int t = pair; t < total && ok; t += n_pairs) {
+            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+            const bool second = two(ti.m);
+            const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
+            const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
+            const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + CH * BK);
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const uint32_t stage = it % STAGES;
+                if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u, abort_flag)) {
+                    give_up(c, a.status);
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
+                uint8_t* s = smem + stage * STAGE_BYTES;
+                if (tc::elect_one()) {
                     if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
                     tc::tma_load_2d_pair(s, &tmA, bar, kb * BK, w0, pol_w);
                     if (second) tc::tma_load_2d_pair(s + A_BYTES, &tmA, bar, kb * BK, w1, pol_w);
                     tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
                                          ti.row0 + rank * CH, pol_x);
-                    issued[stage] = true;
-                    parity[stage] = phase;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
+                __syncwarp();
             }
-            // drain: this CTA's copies have landed (the even CTA's full barrier saw
-            // every byte of both CTAs when its last phase completed)
-            const int zero = 0;
-            for (int s = 0; s < STAGES; ++s)
-                if (issued[s] && !tc::mbar_wait(leader ? &c.full[s] : &c.empty[s], parity[s], &zero))
-                    atomicExch(a.status, MOE_ERR_TIMEOUT);
+        }
+        // drain: this CTA's copies have landed (the even CTA's full barrier saw
+        // every byte of both CTAs when its last phase completed)
+        const int zero = 0;
+        for (uint32_t i = it < STAGES ? 0 : it - STAGES; i < it; ++i) {
+            const uint32_t stage = i % STAGES;
+            if (!tc::mbar_wait(leader ? &c.full[stage] : &c.empty[stage], (i / STAGES) & 1u, &zero))
+                atomicExch(a.status, MOE_ERR_TIMEOUT);
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ---------------- MMA issuer (even CTA): 256 weight rows x 32 tokens, twice
             const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, NM);
-            int stage = 0;
-            uint32_t phase = 0, blk = 0;
+            uint32_t blk = 0;
             bool ok = true;
             for (int t = pair; t < total && ok; t += n_pairs) {
-                const bool second = two(tile_of<NM>(c.tab, a.G, t).m);
+                const bool second = two((int)tc::uniform(tile_of<NM>(c.tab, a.G, t).m));
                 for (int kb = 0; kb < KB; ++kb, ++blk) {
-                    const uint32_t as = blk % ACC;
-                    if (!tc::mbar_wait_hot(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
-                        !tc::mbar_wait_hot(&c.full[stage], phase, abort_flag)) {
+                    const uint32_t as = blk % ACC, stage = blk % STAGES;
+                    if (!tc::mbar_wait_warp(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
+                        !tc::mbar_wait_warp(&c.full[stage], (blk / STAGES) & 1u, abort_flag)) {
                         give_up(c, a.status);
                         ok = false;
                         break;
@@ -197,23 +190,23 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     tc::fence_after_sync();
                     const uint32_t d = tmem_base + as * COLS;
                     const uint32_t w = tc::smem_u32(smem + stage * STAGE_BYTES);
+                    if (tc::elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k) {
-                        const uint64_t x = tc::desc_sw128(w + 2 * A_BYTES + k * 32);
-                        tc::mma_e4m3_pair(d, tc::desc_sw128(w + k * 32), x, idesc, k > 0);
-                        if (second)
-                            tc::mma_e4m3_pair(d + NM, tc::desc_sw128(w + A_BYTES + k * 32), x,
-                                              idesc, k > 0);
+                        for (int k = 0; k < BK / 32; ++k) {
+                            const uint64_t x = tc::desc_sw128(w + 2 * A_BYTES + k * 32);
+                            tc::mma_e4m3_pair(d, tc::desc_sw128(w + k * 32), x, idesc, k > 0);
+                            if (second)
+                                tc::mma_e4m3_pair(d + NM, tc::desc_sw128(w + A_BYTES + k * 32), x,
+                                                  idesc, k > 0);
+                        }
+                        tc::mma_commit_pair(&c.empty[stage], 0x3);
+                        tc::mma_commit_pair(&c.acc_full[as], 0x3);
                     }
-                    tc::mma_commit_pair(&c.empty[stage], 0x3);
-                    tc::mma_commit_pair(&c.acc_full[as], 0x3);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    __syncwarp();
                 }
             }
-            tc::mma_commit_pair(&c.drain, 0x1);
+            if (tc::elect_one()) tc::mma_commit_pair(&c.drain, 0x1);
+            __syncwarp();
             const int zero = 0;
             if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
         }
@@ -274,7 +267,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         uint8_t* tile = epi + grp * (EPI_BYTES / 2);
         uint32_t blk = 0;
         for (int t = pair; t < total; t += n_pairs) {
-            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
             const int left = ti.len - grp * CH;  // valid tokens of this group
             const long tok0 = ti.row0 + grp * CH;
             const bool second = two(ti.m);

@@ -62,7 +62,7 @@ namespace {
 
 // At most kFewRows rows a group on average: the kernel with the weight rows in
 // the MMA's M.
-constexpr long kFewRows = 16;
+constexpr long kFewRows = 64;
 bool few(const BlockGemm& p) { return (long)p.M <= kFewRows * p.G; }
 
 }  // namespace

@@ -3,23 +3,35 @@
 //
 // A pair tile is 256 tokens (the MMA's M, 128 a CTA) times 256 weight rows (its N,
 // each CTA staging 128 of them): 32 KB through shared memory per CTA and block
-// of 128 columns, four K = 32 MMAs into one of two 256-column TMEM accumulators
-// that start from zero. A thread of the promotion owns one token and 128 of the
-// tile's columns: the block's factor sx[token] sw[rows] is one register for all
-// of them (two in gate_up), and the sum of a block is one tcgen05.ld and one
-// fused multiply-add per value. (With the weight rows in M and the tokens in N
-// the factors differ per column and come from shared memory, 16 bytes per 4
-// values and thread: the product 8192 x 8192 x 4096 took 706 us that way.)
+// of 128 columns. A block's sums start from zero in one of two 256-column TMEM
+// accumulators, each handed over in two halves of 128 columns. A thread of the
+// promotion owns one token and 64 of the tile's columns: the block's factor
+// sx[token] sw[rows] is one register for all of them (two in gate_up), and the
+// sum of a block is one fused multiply-add per value. (With the weight rows in M
+// and the tokens in N the factors differ per column and come from shared memory,
+// 16 bytes per 4 values and thread: the product 8192 x 8192 x 4096 took 706 us
+// that way.)
 //
-// gate_up: columns 0-127 are the gate rows of one 128-feature block (staged by
-// the even CTA), 128-255 its up rows (the odd CTA). A thread holds 64 gate and
-// the same 64 up values of its token, so SiLU(g) u, the token's largest |h| and
-// the codes need no exchange but one float between its two threads.
+// gate_up: the even CTA stages the gate rows of one 128-feature block, the odd
+// CTA its up rows; a half holds 64 features' gate columns, then their up columns.
+// A thread holds 32 gate and the same 32 up values of its token, so SiLU(g) u, the
+// token's largest |h| and the codes need no exchange but one float from each of
+// the token's four threads.
 //
-// Per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM owner (+ MMA issuer in
-// the even CTA), warp 2 the factors (a ring in shared memory), warps 4-11 promotion and epilogue, in two groups of four (one
-// warp per 32 TMEM lanes) with half of the columns each. The promotion's threads
-// hold 128 accumulators, so the first four warps hand registers over
+// What bounds it: the hand-over of the accumulators (MMA, commit, read, arrive, next
+// MMA), about 900 cycles per block against 512 of MMAs; more TMEM than there is
+// would hide it. Measured steps, product 8192 x 8192 x 4096: factors loaded by the
+// promotion itself 509 us, from a ring in shared memory 360 us; issuing warps with
+// warp-uniform control flow (the MMA warp alone had needed 1000 cycles a block), the
+// factors waited for once in 4 blocks and four promotion groups in place of two with
+// 128 columns a thread 346 us; halves with an issuing warp each 305 us. 128 weight
+// rows a tile with four accumulators in flight: 507 us.
+//
+// Per CTA (640 threads): warp 0 TMA producer, warps 1 and 3 (even CTA) MMA issuers of
+// one half each, warp 1 also TMEM owner, warp 2 the factors (a ring in shared
+// memory), warps 4-19 promotion and epilogue in four groups (one warp per 32 TMEM
+// lanes; groups 0 and 1 the first half, 2 and 3 the second). The promotion's
+// threads hold 96 values, so the first four warps hand registers over
 // (setmaxnreg). All waits are bounded.
 #include "block_tile.cuh"
 
@@ -32,30 +44,33 @@ constexpr int NM = 2 * BM;             // tokens per pair tile
 constexpr int STAGE_BYTES = 2 * BM * BK;
 constexpr int STAGES = 6;
 constexpr int COLS = 256;              // TMEM columns per block
-constexpr int PROMO_WARP = 4;          // the first of 8
-constexpr int THREADS = 32 * (PROMO_WARP + 8);
-constexpr int CH = 64;                 // columns per tcgen05.ld
+constexpr int GROUPS = 4;              // promotion groups of 4 warps
+constexpr int PROMO_WARP = 4;          // the first of 16
+constexpr int THREADS = 32 * (PROMO_WARP + 4 * GROUPS);
+constexpr int CH = 32;                 // columns per tcgen05.ld
 constexpr int SCALE_WARP = 2;
-constexpr int SLOTS = 8;               // factor ring
-constexpr int EPI_COLS = 32;           // columns per pass of the store staging
-constexpr int EPI_BYTES = 8 * 32 * EPI_COLS * 2;  // [32 tokens][32 columns] bf16 per warp
-// registers a thread: 168 at launch; 3 * 168 = 72 + 2 * 216
-constexpr int REGS_FEW = 72, REGS_MANY = 216;
-static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
+constexpr int FB = 4;                  // blocks per slot of the factor ring
+constexpr int SLOTS = 2;
+constexpr int EPI_COLS = 16;           // columns per pass of the store staging
+constexpr int EPI_BYTES = 4 * GROUPS * 32 * EPI_COLS * 2;  // [32 tokens][16 columns] bf16 per warp
+// registers a thread: 96 at launch; 5 * 96 = 32 + 4 * 112
+constexpr int REGS_FEW = 32, REGS_MANY = 112;
+static_assert(REGS_FEW + GROUPS * REGS_MANY == (1 + GROUPS) * 96, "no more than the launch gave");
 
 struct Ctrl {
     uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
     uint64_t empty[STAGES];   // both CTAs: the pair MMAs finished reading the stage
-    uint64_t acc_full[2];     // both CTAs: a block's sums are in TMEM
-    uint64_t acc_empty[2];    // even CTA: every promotion warp of both CTAs has read them
+    // of each half of the columns:
+    uint64_t acc_full[2][2];   // both CTAs: a block's sums are in TMEM
+    uint64_t acc_empty[2][2];  // even CTA: the promotion warps of both CTAs have read them
     uint64_t sc_full[SLOTS];
     uint64_t sc_empty[SLOTS];
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     TileTable tab;
-    float amax[2][BM];        // gate_up: a token's largest |h| in each group's columns
-    float factor[SLOTS][2][BM];  // sx[token] * sw of the columns 0-127 and 128-255
+    float amax[GROUPS][BM];   // gate_up: a token's largest |h| in each group's columns
+    float factor[SLOTS][FB][2][BM];  // sx[token] * sw of the columns 0-127 and 128-255
 };
 constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + (int)sizeof(Ctrl);
 static_assert(SMEM <= 232448, "fits in 227 KB");
@@ -78,11 +93,10 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                   const Args a) {
     pdl_launch_and_wait();
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // stays a shared pointer
     uint8_t* epi = smem + STAGES * STAGE_BYTES;
     Ctrl& c = *reinterpret_cast<Ctrl*>(epi + EPI_BYTES);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)(tc::cluster_ctarank() & 1u);
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
@@ -100,17 +114,19 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         if (lane == 0) {
             for (int s = 0; s < STAGES; ++s) {
                 tc::mbar_init(&c.full[s], 1);
-                tc::mbar_init(&c.empty[s], 1);
+                tc::mbar_init(&c.empty[s], 2);
             }
             for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(&c.acc_full[i], 1);
-                tc::mbar_init(&c.acc_empty[i], 2 * 8);
+                for (int h = 0; h < 2; ++h) {
+                    tc::mbar_init(&c.acc_full[i][h], 1);
+                    tc::mbar_init(&c.acc_empty[i][h], 2 * 4 * GROUPS / 2);
+                }
             }
             for (int i = 0; i < SLOTS; ++i) {
                 tc::mbar_init(&c.sc_full[i], 1);
-                tc::mbar_init(&c.sc_empty[i], 8);
+                tc::mbar_init(&c.sc_empty[i], 4 * GROUPS);
             }
-            tc::mbar_init(&c.drain, 1);
+            for (int h = 0; h < 2; ++h) tc::mbar_init(&c.drain[h], 1);
             tc::fence_mbar_init();
         }
         __syncwarp();
@@ -120,8 +136,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     tc::fence_before_sync();
     tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc::fence_after_sync();
-    const uint32_t tmem_base = c.tmem_base;
-    const int total = c.tab.total;
+    const uint32_t tmem_base = tc::uniform(c.tmem_base);
+    const int total = (int)tc::uniform(c.tab.total);
     const volatile int* abort_flag = &c.abort;
 
     if (warp >= PROMO_WARP) {
@@ -130,15 +146,17 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         const int quad = warp & 3, grp = (warp - PROMO_WARP) >> 2;
         const int row = quad * 32 + lane;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
-        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0]), 0);
-        // the two chunks of this thread's columns: gate_up 64 gate columns and their
-        // up ones
-        const int col0 = GATE_UP ? grp * CH : grp * 2 * CH;
-        const int col1 = GATE_UP ? 2 * CH + grp * CH : grp * 2 * CH + CH;
+        const int half = grp >> 1, side = grp & 1;
+        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0][half]), 0);
+        // the two chunks of this thread's columns (half h of them: the h-th 64 rows of
+        // the even CTA's weights, then of the odd one's): gate_up 32 gate columns and
+        // their up ones, else 64 columns of one CTA's rows
+        const uint32_t col0 = half * 128 + side * (GATE_UP ? CH : 2 * CH);
+        const uint32_t col1 = col0 + (GATE_UP ? 2 * CH : CH);
         const int nb_n = (a.N + 127) / 128;
-        uint32_t blk = 0;
+        uint32_t blk = 0, batch = 0;
         for (int t = pair; t < total; t += n_pairs) {
-            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
             const int tok = rank * BM + row;                     // token within the tile
             const bool mine = tok < ti.len;
             const bool active = rank * BM + quad * 32 < ti.len;  // any token of the warp
@@ -149,38 +167,38 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 for (int j = 0; j < CH / 2; ++j) acc[i][j] = 0;
             bool ok = true;
             for (int kb = 0; kb < KB; ++kb, ++blk) {
-                const uint32_t as = blk & 1u, slot = blk % SLOTS;
-                ok = tc::mbar_wait_hot(&c.sc_full[slot], (blk / SLOTS) & 1u, abort_flag) &&
-                     tc::mbar_wait_hot(&c.acc_full[as], (blk >> 1) & 1u, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);  // the warp stays together
+                const uint32_t as = blk & 1u, slot = batch % SLOTS;
+                if (kb % FB == 0)
+                    ok = tc::mbar_wait_warp(&c.sc_full[slot], (batch / SLOTS) & 1u, abort_flag);
+                ok = ok && tc::mbar_wait_warp(&c.acc_full[as][half], (blk >> 1) & 1u, abort_flag);
                 if (!ok) break;
+                float f0 = 0.f, f1 = 0.f;
+                uint32_t d[CH];
                 if (active) {
                     tc::fence_after_sync();
                     const uint32_t tb = lane_base + as * COLS;
-                    uint32_t d[CH];
-                    tc::tmem_ld64(tb + col0, d);
-                    const float f0 = c.factor[slot][GATE_UP ? 0 : grp][row];
-                    const float f1 = GATE_UP ? c.factor[slot][1][row] : f0;
+                    tc::tmem_ld32(tb + col0, d);
+                    f0 = c.factor[slot][kb % FB][GATE_UP ? 0 : side][row];
+                    f1 = GATE_UP ? c.factor[slot][kb % FB][1][row] : f0;
                     tc::tmem_ld_wait();
                     tc::tmem_loaded(d);
                     promote(acc[0], d, f0);
-                    tc::tmem_ld64(tb + col1, d);
+                    tc::tmem_ld32(tb + col1, d);
                     tc::tmem_ld_wait();
                     tc::tmem_loaded(d);
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
-                        tc::mbar_arrive(&c.sc_empty[slot]);
-                    }
-                    promote(acc[1], d, f1);
-                } else if (lane == 0) {
-                    tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
-                    tc::mbar_arrive(&c.sc_empty[slot]);
                 }
+                const bool last = kb % FB == FB - 1 || kb + 1 == KB;
+                tc::fence_before_sync();
+                if (tc::elect_one()) {
+                    tc::mbar_arrive_cluster_read(acc_empty0 + as * 16);
+                    if (last) tc::mbar_arrive(&c.sc_empty[slot]);
+                }
+                __syncwarp();
+                batch += last;
+                if (active) promote(acc[1], d, f1);
             }
             if constexpr (GATE_UP) {
-                // h in acc[0]; the token's largest |h| over both groups' columns
+                // h in acc[0]; the token's largest |h| over all groups' columns
                 uint32_t mx = 0;
 #pragma unroll
                 for (int j = 0; j < CH; j += 2) {
@@ -191,56 +209,58 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 }
                 c.amax[grp][row] = f32_from_bits(mx);
                 // (a warp that gave up takes the others with it)
-                if (tc::bar_any(1, 256, !ok)) {
+                if (tc::bar_any(1, 128 * GROUPS, !ok)) {
                     give_up(c, a.status);
                     break;
                 }
-                const BlockScale b =
-                    block_scale(f32_from_bits(max(mx, f32_bits(c.amax[grp ^ 1][row]))));
+                const BlockScale b = block_scale(f32_from_bits(
+                    max(max(f32_bits(c.amax[0][row]), f32_bits(c.amax[1][row])),
+                        max(f32_bits(c.amax[2][row]), f32_bits(c.amax[3][row])))));
                 if (mine) {
                     const long r = ti.row0 + tok;
                     if (grp == 0) a.out_scales[r * nb_n + ti.m] = b.scale;
                     uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + r * a.N +
-                                                        ti.m * 128 + grp * 64);
+                                                        ti.m * 128 + grp * CH);
 #pragma unroll
                     for (int q = 0; q < CH / 16; ++q) {
                         uint32_t w[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
                             const int j = q * 16 + v * 4;
-                            w[v] = e4m3x2_of(block_quotient(b, value_at(acc[0], j)),
-                                             block_quotient(b, value_at(acc[0], j + 1))) |
-                                   (e4m3x2_of(block_quotient(b, value_at(acc[0], j + 2)),
-                                              block_quotient(b, value_at(acc[0], j + 3)))
+                            const auto& h = acc[0];
+                            w[v] = e4m3x2_of(block_quotient(b, value_at(h, j)),
+                                             block_quotient(b, value_at(h, j + 1))) |
+                                   (e4m3x2_of(block_quotient(b, value_at(h, j + 2)),
+                                              block_quotient(b, value_at(h, j + 3)))
                                     << 16);
                         }
                         o[q] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
-                tc::bar_sync(1, 256);  // amax is read before the next tile's
+                tc::bar_sync(1, 128 * GROUPS);  // amax is read before the next tile's
             } else {
                 if (!ok) {
                     give_up(c, a.status);
                     break;
                 }
                 if (!active) continue;
-                const int n0 = ti.m * COLS + grp * 128;          // first output column
+                const int n0 = ti.m * COLS + side * 128 + half * 2 * CH;  // first output column
                 const int rows = ti.len - rank * BM - quad * 32; // tokens of this warp
                 const long r0 = ti.row0 + rank * BM + quad * 32;
                 if (!OUT_F32 && a.N % 8 == 0) {
-                    // 32 columns at a time through the warp's [32 tokens][32 columns]
-                    // tile, 16-byte pieces swizzled by the token: 64-byte row segments
-                    // go out four lanes a row
+                    // 16 columns at a time through the warp's [32 tokens][16 columns]
+                    // tile, its 16-byte halves swapped for every other four tokens (no
+                    // bank conflicts): whole 32-byte sectors go out, two lanes a row
                     uint4* st = reinterpret_cast<uint4*>(
-                        epi + (warp - PROMO_WARP) * (EPI_BYTES / 8));
+                        epi + (warp - PROMO_WARP) * (EPI_BYTES / (4 * GROUPS)));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2 * CH / EPI_COLS; ++i) {
                         __syncwarp();  // the previous pass is read
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const auto& v = acc[i >> 1];
-                            const int j = (i & 1) * 32 + q * 8;
-                            st[lane * 4 + (q ^ ((lane >> 1) & 3))] = make_uint4(
+                        for (int q = 0; q < 2; ++q) {
+                            const auto& v = acc[i / (CH / EPI_COLS)];
+                            const int j = (i % (CH / EPI_COLS)) * EPI_COLS + q * 8;
+                            st[lane * 2 + (q ^ ((lane >> 2) & 1))] = make_uint4(
                                 pack_bf16x2(value_at(v, j), value_at(v, j + 1)),
                                 pack_bf16x2(value_at(v, j + 2), value_at(v, j + 3)),
                                 pack_bf16x2(value_at(v, j + 4), value_at(v, j + 5)),
@@ -248,13 +268,13 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int n = q * 8 + (lane >> 2), ch = lane & 3;
-                            const int col = n0 + i * 32 + ch * 8;
+                        for (int q = 0; q < 2; ++q) {
+                            const int n = q * 16 + (lane >> 1), ch = lane & 1;
+                            const int col = n0 + i * EPI_COLS + ch * 8;
                             if (n < rows && col < a.N)
                                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
                                                           (r0 + n) * a.N + col) =
-                                    st[n * 4 + (ch ^ ((n >> 1) & 3))];
+                                    st[n * 2 + (ch ^ ((n >> 2) & 1))];
                         }
                     }
                 } else if (mine) {
@@ -277,95 +297,93 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     } else {
         tc::regs_dec<REGS_FEW>();
         if (warp == 0) {
-            if (lane == 0) {
-                // ---------------- producer: this CTA's 128 tokens and 128 weight rows
-                const uint64_t pol_w = tc::policy_evict_first();
-                const uint64_t pol_x = tc::policy_evict_last();
-                int stage = 0;
-                uint32_t phase = 0;
-                uint32_t parity[STAGES] = {};
-                bool issued[STAGES] = {};
-                bool ok = true;
-                for (int t = pair; t < total && ok; t += n_pairs) {
-                    const Tile ti = tile_of<NM>(c.tab, a.G, t);
-                    // the rows that exist, in 16-row boxes (what the rest of the stage
-                    // holds only reaches TMEM lanes that nobody reads)
-                    const int r0 = (min(ti.len, BM) + 15) & ~15;
-                    const int r1 = (max(ti.len - BM, 0) + 15) & ~15;
-                    const int rows = leader ? r0 : r1;
-                    const int w0 = ti.g * a.w_rows +
-                                   (GATE_UP ? ti.m * BM + rank * a.N : ti.m * COLS + rank * BM);
-                    const uint32_t bytes = (uint32_t)(2 * BM + r0 + r1) * BK;
-                    for (int kb = 0; kb < KB; ++kb) {
-                        if (!tc::mbar_wait_hot(&c.empty[stage], phase ^ 1u, abort_flag)) {
-                            give_up(c, a.status);
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
-                        uint8_t* s = smem + stage * STAGE_BYTES;
+            // ---------------- producer: this CTA's 128 tokens and 128 weight rows
+            const uint64_t pol_w = tc::policy_evict_first();
+            const uint64_t pol_x = tc::policy_evict_last();
+            uint32_t it = 0;  // blocks loaded
+            bool ok = true;
+            for (int t = pair; t < total && ok; t += n_pairs) {
+                const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+                // the rows that exist, in 16-row boxes (what the rest of the stage
+                // holds only reaches TMEM lanes that nobody reads)
+                const int r0 = (min(ti.len, BM) + 15) & ~15;
+                const int r1 = (max(ti.len - BM, 0) + 15) & ~15;
+                const int rows = leader ? r0 : r1;
+                const uint32_t bytes = (uint32_t)(2 * BM + r0 + r1) * BK;
+                const int w0 = ti.g * a.w_rows +
+                               (GATE_UP ? ti.m * BM + rank * a.N : ti.m * COLS + rank * BM);
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const uint32_t stage = it % STAGES;
+                    if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u,
+                                            abort_flag)) {
+                        give_up(c, a.status);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
+                    uint8_t* s = smem + stage * STAGE_BYTES;
+                    if (tc::elect_one()) {
                         if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
                         tc::tma_load_2d_pair(s + BM * BK, &tmA, bar, kb * BK, w0, pol_w);
                         load_tokens(s, tmB, bar, kb * BK, ti.row0 + rank * BM, rows, pol_x);
-                        issued[stage] = true;
-                        parity[stage] = phase;
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
                     }
+                    __syncwarp();
                 }
-                // drain: this CTA's copies have landed (the even CTA's full barrier saw
-                // every byte of both CTAs when its last phase completed)
-                const int zero = 0;
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued[s] &&
-                        !tc::mbar_wait(leader ? &c.full[s] : &c.empty[s], parity[s], &zero))
-                        atomicExch(a.status, MOE_ERR_TIMEOUT);
             }
-        } else if (warp == 1) {
-            if (lane == 0 && leader) {
-                // ---------------- MMA issuer (even CTA): 256 tokens x 256 weight rows
-                const uint32_t idesc = tc::idesc_e4m3_f32(NM, COLS);
-                int stage = 0;
-                uint32_t phase = 0, blk = 0;
+            // drain: this CTA's copies have landed (the even CTA's full barrier saw
+            // every byte of both CTAs when its last phase completed)
+            const int zero = 0;
+            for (uint32_t i = it < STAGES ? 0 : it - STAGES; i < it; ++i) {
+                const uint32_t stage = i % STAGES;
+                if (!tc::mbar_wait(leader ? &c.full[stage] : &c.empty[stage], (i / STAGES) & 1u,
+                                   &zero))
+                    atomicExch(a.status, MOE_ERR_TIMEOUT);
+            }
+        } else if (warp == 1 || warp == 3) {
+            if (leader) {
+                // ---------------- MMA issuers (even CTA): 256 tokens x 128 weight rows,
+                // warp 1 the first half of the columns, warp 3 the second
+                const uint32_t half = warp >> 1;
+                const uint32_t idesc = tc::idesc_e4m3_f32(NM, COLS / 2);
+                uint32_t blk = 0;
                 bool ok = true;
                 for (int t = pair; t < total && ok; t += n_pairs) {
                     for (int kb = 0; kb < KB; ++kb, ++blk) {
-                        const uint32_t as = blk & 1u;
-                        if (!tc::mbar_wait_hot(&c.acc_empty[as], ((blk >> 1) & 1u) ^ 1u,
-                                               abort_flag) ||
-                            !tc::mbar_wait_hot(&c.full[stage], phase, abort_flag)) {
+                        const uint32_t as = blk & 1u, stage = blk % STAGES;
+                        if (!tc::mbar_wait_warp(&c.acc_empty[as][half], ((blk >> 1) & 1u) ^ 1u,
+                                                abort_flag) ||
+                            !tc::mbar_wait_warp(&c.full[stage], (blk / STAGES) & 1u, abort_flag)) {
                             give_up(c, a.status);
                             ok = false;
                             break;
                         }
                         tc::fence_after_sync();
                         const uint32_t x = tc::smem_u32(smem + stage * STAGE_BYTES);
+                        const uint32_t w = x + BM * BK + half * (BM / 2) * BK;
+                        if (tc::elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < BK / 32; ++k)
-                            tc::mma_e4m3_pair(tmem_base + as * COLS, tc::desc_sw128(x + k * 32),
-                                              tc::desc_sw128(x + BM * BK + k * 32), idesc, k > 0);
-                        tc::mma_commit_pair(&c.empty[stage], 0x3);
-                        tc::mma_commit_pair(&c.acc_full[as], 0x3);
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1u;
+                            for (int k = 0; k < BK / 32; ++k)
+                                tc::mma_e4m3_pair(tmem_base + as * COLS + half * (COLS / 2),
+                                                  tc::desc_sw128(x + k * 32),
+                                                  tc::desc_sw128(w + k * 32), idesc, k > 0);
+                            tc::mma_commit_pair(&c.acc_full[as][half], 0x3);
+                            tc::mma_commit_pair(&c.empty[stage], 0x3);
                         }
+                        __syncwarp();
                     }
                 }
-                tc::mma_commit_pair(&c.drain, 0x1);
+                if (tc::elect_one()) tc::mma_commit_pair(&c.drain[half], 0x1);
+                __syncwarp();
                 const int zero = 0;
-                if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
+                if (!tc::mbar_wait(&c.drain[half], 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
             }
         } else if (warp == SCALE_WARP) {
             // ---------------- factors: per block sx[token] * sw of each half of the
-            // columns, 4 tokens a lane, U blocks loaded at a time; the ring runs ahead
-            // of the promotion, over tile borders too
-            constexpr int U = 4;
+            // columns, 4 tokens a lane, FB blocks a slot; the ring runs ahead of the
+            // promotion, over tile borders too
             const int nb_n = (a.N + 127) / 128;
             const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
-            uint32_t blk = 0;
+            uint32_t batch = 0;
             bool ok = true;
             for (int t = pair; t < total && ok; t += n_pairs) {
                 const Tile ti = tile_of<NM>(c.tab, a.G, t);
@@ -375,10 +393,10 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 const int nb1 = GATE_UP ? nb_n + ti.m : min(ti.m * 2 + 1, nb_n - 1);
                 const float* sw0 = a.sw + ((size_t)ti.g * sw_rows + nb0) * KB;
                 const float* sw1 = a.sw + ((size_t)ti.g * sw_rows + nb1) * KB;
-                for (int k0 = 0; k0 < KB && ok; k0 += U) {
-                    float x[4][U], w0[U], w1[U];
+                for (int k0 = 0; k0 < KB; k0 += FB, ++batch) {
+                    float x[4][FB], w0[FB], w1[FB];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int u = 0; u < FB; ++u) {
                         const bool in = k0 + u < KB;
                         w0[u] = in ? sw0[k0 + u] : 0.f;
                         w1[u] = in ? sw1[k0 + u] : 0.f;
@@ -387,26 +405,23 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                             x[i][u] = in && 32 * i < left ? sxp[(size_t)(32 * i) * KB + k0 + u]
                                                           : 0.f;
                     }
+                    const uint32_t slot = batch % SLOTS;
+                    ok = tc::mbar_wait_hot(&c.sc_empty[slot], ((batch / SLOTS) & 1u) ^ 1u,
+                                           abort_flag);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) {
+                        give_up(c, a.status);
+                        break;
+                    }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (k0 + u >= KB || !ok) continue;
-                        const uint32_t slot = blk % SLOTS;
-                        ok = tc::mbar_wait_hot(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u,
-                                               abort_flag);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) {
-                            give_up(c, a.status);
-                            continue;
-                        }
+                    for (int u = 0; u < FB; ++u)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            c.factor[slot][0][lane + 32 * i] = x[i][u] * w0[u];
-                            c.factor[slot][1][lane + 32 * i] = x[i][u] * w1[u];
+                            c.factor[slot][u][0][lane + 32 * i] = x[i][u] * w0[u];
+                            c.factor[slot][u][1][lane + 32 * i] = x[i][u] * w1[u];
                         }
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
-                        ++blk;
-                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
                 }
             }
         }

@@ -92,6 +92,12 @@ __device__ __forceinline__ Tile tile_of(const TileTable& c, int G, int t) {
     return Tile{lo, m, c.off[lo] + j * NM, min(NM, rows - j * NM)};
 }
 
+// The tile in uniform registers (all lanes hold the same one).
+__device__ __forceinline__ Tile uniform_tile(const Tile& t) {
+    return Tile{(int)tc::uniform(t.g), (int)tc::uniform(t.m), (int)tc::uniform(t.row0),
+                (int)tc::uniform(t.len)};
+}
+
 // `rows` (a multiple of 16, at most 128) token rows from `row` on, as at most
 // four boxes, completing on the even CTA's barrier.
 __device__ __forceinline__ void load_tokens(uint8_t* dst, const TokenMaps& tm, uint32_t bar,

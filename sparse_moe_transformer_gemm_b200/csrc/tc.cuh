@@ -22,6 +22,25 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// A value that is the same in all lanes, in a form the compiler knows to be: with
+// warp-uniform control flow and operands, the instructions that take uniform
+// registers (tcgen05, TMA, mbarrier) need no per-instruction conversions, which
+// cost an issuing thread about 100 cycles each.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -83,6 +102,12 @@ __device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
     for (int i = 0; i < POLLS; ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_for(bar, parity, abort_flag, kWaitNs);
+}
+
+// mbar_wait_hot by a converged warp: all lanes get the same answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
+                                               const volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, abort_flag));
 }
 
 // ------------------------------------------------------------------ TMA
