@@ -7,19 +7,18 @@
 //   the topk_group best groups stay; the k largest c in them are chosen
 //   w_j = scale * s_j (/ sum of the chosen s)
 //
-// One warp per token: lane l holds the experts l, l + 32, ... (E <= 256). The
-// choice is k rounds of a warp-wide argmax on order-preserving integer keys.
+// One warp per token with up to 8 experts a lane (E <= 256). The scores increase
+// with the logit, so without a bias the experts are ranked by the logits
+// themselves; with one, and for sums of two scores, by fp32 evaluations. A token's
+// common path is choose_packed on 32-bit keys. Where a comparison that decides
+// something is closer than the bits cut off or the evaluation's error, the token
+// is chosen once more exactly, with scores in fp64: about one token in 500 with a
+// bias, one in 50000 without.
 //
-// Ranking. The scores increase with the logit, so without a bias the experts
-// are ranked by the logits themselves, exactly. With a bias, and for sums of
-// two scores, the values are computed in fp32 and every comparison that decides
-// something (consecutive choices, the first expert left out, the last group
-// kept against the best one dropped) has to be wider than the evaluation's
-// error bound; a token where one is not runs once more in fp64 (about one token
-// in 500 at E = 256). fp64 for every token would take the fp64 pipe several
-// times longer than reading the logits takes.
-//
-// Bound: the logits, 4 T E bytes, against about 500 instructions per token.
+// Bound: about 450 instructions per token against 4 E bytes read. Measured, E =
+// 256, top-8, T = 16384: 13.3 us without a bias or groups (reading the logits
+// takes 2.6); biased, 4 of 8 groups by their two best: 30 us, of which about 7
+// are the latency of the few exact tokens. T = 64: 2.8 us, the launch's.
 #include <float.h>
 
 #include "common.cuh"
@@ -31,6 +30,7 @@ namespace {
 constexpr int WARPS = 4;      // tokens per CTA
 constexpr int Q = 8;          // experts per lane
 constexpr int PAD_E = 256 + 8;
+constexpr int kCtasPerSm = 8;  // persistent CTAs
 
 struct SelectArgs {
     const float* logits;
@@ -53,53 +53,48 @@ __device__ __forceinline__ unsigned long long key_of(double v) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
     return (b >> 63) ? ~b : (b | (1ull << 63));
 }
-__device__ __forceinline__ double value_of(unsigned long long k) {
-    return __longlong_as_double((long long)((k >> 63) ? (k ^ (1ull << 63)) : ~k));
-}
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) {
     return __reduce_max_sync(0xffffffffu, k);
 }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const unsigned long long p = __shfl_xor_sync(0xffffffffu, k, o);
-        k = p > k ? p : k;
-    }
-    return k;
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+    const uint32_t lo =
+        __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return ((unsigned long long)hi << 32) | lo;
 }
 template <typename V>
 __device__ __forceinline__ V warp_max_value(V v) { return value_of(warp_max(key_of(v))); }
 
-__device__ __forceinline__ float warp_total(float v) { return warp_sum(v); }
 __device__ __forceinline__ double warp_total(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// Scores (softmax: before the division by the sum; z - max for z). Errors of
-// the fp32 forms are below 1e-6 of 1 + score: the fast exponential is within
-// |z| 2^-24 + 2^-22 of its value, which the score's slope in z turns into at
-// most that.
+// The fp32 scores (softmax: before the division by the sum; z - max for z). The
+// fast exponential is within |z| 2^-24 + 2^-22 of its value, which the sigmoid's
+// slope s (1 - s) turns into at most 8e-8, the fast reciprocal adds 2 ulp, the sum
+// with the bias half of one: together below 4e-7 of 1 + |c|; the softmax's sum and
+// the sqrt-softplus stay below that too. The difference of two of them is
+// certain beyond kScoreError of 1 + |c|, that of two sums beyond twice as much.
+constexpr float kScoreError = 1e-6f;
 __device__ __forceinline__ float score_of(float z, int fn) {
     if (fn == MOE_SCORE_SOFTMAX) return __expf(z);
     if (fn == MOE_SCORE_SQRT_SOFTPLUS)
         return sqrtf(fmaxf(z, 0.f) + log1pf(__expf(-fabsf(z))));
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
-__device__ __noinline__ double score_of(double z, int fn) {
-    if (fn == MOE_SCORE_SOFTMAX) return exp(z);
+__device__ __forceinline__ double score_of(double z, int fn) {
     if (fn == MOE_SCORE_SQRT_SOFTPLUS) return sqrt(fmax(z, 0.0) + log1p(exp(-fabs(z))));
     return 1.0 / (1.0 + exp(-z));
 }
 
-// Whether a > b can be told apart in spite of the evaluation's error (fp64:
-// always taken as it is; two -infinities are a tie that the index decides).
+// Whether a > b can be told apart in spite of the evaluation's error (of sums of
+// two scores; a tie of two -infinities is decided by the index).
 __device__ __forceinline__ bool decided(float a, float b) {
-    return b == -INFINITY || a - b > 4e-6f * (1.0f + fmaxf(fabsf(a), fabsf(b)));
+    return b == -INFINITY || a - b > 2 * kScoreError * (1.0f + fmaxf(fabsf(a), fabsf(b)));
 }
-__device__ __forceinline__ bool decided(double, double) { return true; }
 
 template <typename V>
 struct Scratch {
@@ -112,33 +107,31 @@ union WarpScratch {
     Scratch<double> d;
 };
 
-// One token's choice by one warp; lane j < k gets the j-th expert in `mine`.
-// Returns whether every comparison was wider than the error (uniform).
+// One token's choice by one warp; lane j < k gets the j-th expert in `mine`. V
+// float: no score takes part in a comparison; double: scores in 64 bits. (The
+// score loop is rolled: this runs for single tokens, whose time is mostly that of
+// fetching the instructions.)
 template <typename V>
-__device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q], float zmax,
+__device__ __forceinline__ void choose(const SelectArgs& a, const float (&z)[Q], float zmax,
                                        Scratch<V>& sc, int& mine) {
     using K = decltype(key_of(V()));
     const int lane = threadIdx.x & 31;
     const bool top2 = a.n_group > 1 && a.group_score == MOE_GROUP_TOP2;
     V r[Q], c[Q];  // what experts are ranked by; what groups sum
-    if (a.bias || top2) {
+    if constexpr (sizeof(V) == 8) {
         V total = 1;
         if (a.score_fn == MOE_SCORE_SOFTMAX) {
             V part = 0;
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-                if (lane + 32 * q < a.E) {
-                    c[q] = score_of((V)z[q] - (V)zmax, a.score_fn);
-                    part += c[q];
-                }
-            total = warp_total(part);
+#pragma unroll 1
+            for (int q = 0; q < Q; ++q) part += exp((double)z[q] - (double)zmax);
+            total = warp_total(part);  // (an expert that is out adds 0)
         }
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < Q; ++q) {
             const int e = lane + 32 * q;
-            if (e >= a.E) continue;
-            V s = a.score_fn == MOE_SCORE_SOFTMAX ? c[q] / total : score_of((V)z[q], a.score_fn);
-            if (a.bias) s += (V)cleaned(a.bias[e]);
+            V s = a.score_fn == MOE_SCORE_SOFTMAX ? exp((double)z[q] - (double)zmax) / total
+                                                  : score_of((double)z[q], a.score_fn);
+            if (a.bias && e < a.E) s += (V)cleaned(a.bias[e]);
             c[q] = z[q] == -INFINITY ? (V)-INFINITY : s;
             r[q] = a.bias ? c[q] : (V)z[q];
         }
@@ -149,7 +142,6 @@ __device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q],
     K key[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) key[q] = lane + 32 * q < a.E ? key_of(r[q]) : (K)0;
-    bool sure = true;
 
     if (a.n_group > 1) {
         const int G = a.n_group, n = a.E / G;
@@ -181,7 +173,6 @@ __device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q],
         }
         __syncwarp();
         // a group stays if fewer than topk_group groups are ahead of it
-        K worst_kept = ~(K)0, best_left = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {
             const int g = g0 + lane;
             int ahead = 0;
@@ -190,15 +181,10 @@ __device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q],
                 const V v = sc.group[o];
                 ahead += v > own || (v == own && o < g);
             }
-            const bool keep = g < G && ahead < a.topk_group;
-            const uint32_t bits = __ballot_sync(0xffffffffu, keep);
+            const uint32_t bits =
+                __ballot_sync(0xffffffffu, g < G && ahead < a.topk_group);
             if (lane == 0) sc.kept[g0 >> 5] = bits;
-            const K kk = key_of(own);
-            if (keep) worst_kept = kk < worst_kept ? kk : worst_kept;
-            if (g < G && !keep) best_left = kk > best_left ? kk : best_left;
         }
-        if ((a.bias || top2) && a.topk_group < G)
-            sure = decided(value_of((K)~warp_max((K)~worst_kept)), value_of(warp_max(best_left)));
         __syncwarp();
         // e / n by a multiplication: exact for e < 256 (the error e / 2^16 is
         // below the distance 1 / n >= 1 / 256 to the next integer)
@@ -210,24 +196,15 @@ __device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q],
         }
     }
 
-    // k rounds, and where values are inexact one more for the first one left out
-    const int rounds = a.bias ? a.k + 1 : a.k;
-    V before = 0;
-    for (int j = 0; j < rounds; ++j) {
+    for (int j = 0; j < a.k; ++j) {
         K best = key[0];
         int bq = 0;
 #pragma unroll
         for (int q = 1; q < Q; ++q)
             if (key[q] > best) { best = key[q]; bq = q; }
         const K m = warp_max(best);
-        if (m == 0) break;  // nothing left (uniform)
         const uint32_t e = __reduce_min_sync(0xffffffffu,
                                              best == m ? (uint32_t)(lane + 32 * bq) : 0xffffffffu);
-        if (a.bias) {
-            const V v = value_of(m);
-            if (j > 0) sure = sure && decided(before, v);
-            before = v;
-        }
         if (lane == j) mine = (int)e;
         if ((int)(e & 31u) == lane) {
 #pragma unroll
@@ -235,66 +212,255 @@ __device__ __forceinline__ bool choose(const SelectArgs& a, const float (&z)[Q],
                 if ((int)(e >> 5) == q) key[q] = 0;
         }
     }
-    return sure;
 }
 
-__global__ void __launch_bounds__(WARPS * 32)
-select_kernel(const SelectArgs a) {
-    pdl_launch_and_wait();
-    __shared__ WarpScratch scratch[WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long t = (long)blockIdx.x * WARPS + warp;
-    if (t >= a.T) return;
+// The choice by one warp from its 8 values a lane, in one pass of 32-bit keys: the
+// upper 29 bits of the value's order-preserving key, then 7 - q for the lane's
+// q-th expert (of equal values the earlier one first). Each lane sorts its 8 keys
+// once (19 compare-exchanges); a round is one redux.sync on the lanes' heads and a
+// ballot. Values whose difference is within the cut-off bits or the evaluation's
+// error make the result void (false, uniform): the caller repeats the token
+// exactly. `mine`: 8 * lane + q of this lane's choice.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
+    a = hi;
+    b = lo;
+}
+__device__ __forceinline__ bool choose_packed(uint32_t (&h)[Q], int k, float error, int& mine) {
+    const int lane = threadIdx.x & 31;
+    // a sorting network of 8 (Batcher's odd-even merge), descending
+    exchange(h[0], h[1]); exchange(h[2], h[3]); exchange(h[4], h[5]); exchange(h[6], h[7]);
+    exchange(h[0], h[2]); exchange(h[1], h[3]); exchange(h[4], h[6]); exchange(h[5], h[7]);
+    exchange(h[1], h[2]); exchange(h[5], h[6]);
+    exchange(h[0], h[4]); exchange(h[1], h[5]); exchange(h[2], h[6]); exchange(h[3], h[7]);
+    exchange(h[2], h[4]); exchange(h[3], h[5]);
+    exchange(h[1], h[2]); exchange(h[3], h[4]); exchange(h[5], h[6]);
+    uint32_t key = 0, left_out = 0;  // lane j: the j-th key; the key after the last choice
+    for (int j = 0; j <= k; ++j) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, h[0]);
+        const int winner = __ffs(__ballot_sync(0xffffffffu, h[0] == m)) - 1;
+        if (lane == j) {
+            key = m;
+            mine = winner * Q + 7 - (int)(m & 7u);
+        }
+        left_out = m;
+        if (lane == winner) {
+#pragma unroll
+            for (int q = 0; q < Q - 1; ++q) h[q] = h[q + 1];
+            h[Q - 1] = 0;
+        }
+    }
+    // lane j: its choice against the next one (or the first one left out; 0: none is)
+    uint32_t next = __shfl_down_sync(0xffffffffu, key, 1);
+    if (lane == k - 1) next = left_out;
+    bool sure = (key ^ next) > 7u;  // different keys after the cut are in order
+    if (error > 0.f && next != 0) {
+        const float v = key_value(key & ~7u), u = key_value(next & ~7u);
+        const float big = fmaxf(fabsf(v), fabsf(u));
+        sure = v - u > fmaf(1e-6f, big, error * (1.0f + big));  // (false for two -infinities)
+    }
+    return __all_sync(0xffffffffu, sure || lane >= k);
+}
+
+// Lane j < k: the weight of its expert from that expert's logit zj; z and zmax (the
+// softmax's reference) are the token's. Where the weights are divided by their
+// sum, a common factor is free: the softmax takes the largest chosen logit as its
+// reference, and scores of logits so small that fp32 would lose them (sigmoid(z)
+// = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are taken relative to the
+// largest one's.
+__device__ __forceinline__ float weight_of(const SelectArgs& a, int fn, const float (&z)[Q],
+                                           float zmax, float zj) {
+    float s;
+    if (a.renorm) {
+        const float zc = warp_max_value(zj);
+        if (fn == MOE_SCORE_SOFTMAX)
+            s = zc > -INFINITY ? expf(zj - zc) : 0.f;
+        else if (zc < -80.f)
+            s = zc > -INFINITY ? expf(fn == MOE_SCORE_SIGMOID ? zj - zc : 0.5f * (zj - zc)) : 0.f;
+        else
+            s = score_value(zj, fn);
+        const float den = warp_sum(s);
+        return den > 0.f ? a.scale * __fdividef(s, den) : 0.f;
+    }
+    if (fn != MOE_SCORE_SOFTMAX) return a.scale * score_value(zj, fn);
+    float part = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) part += expf(z[q] - zmax);  // 0 for an expert that is out
+    const float den = warp_sum(part);
+    return den > 0.f ? a.scale * (expf(zj - zmax) / den) : 0.f;
+}
+
+__device__ __forceinline__ float largest(const float (&z)[Q]) {
+    float m = z[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) m = fmaxf(m, z[q]);
+    m = warp_max_value(m);
+    return m == -INFINITY ? 0.f : m;  // every expert is out: all scores 0
+}
+
+// A token's choice and weights without a cut: logits as they are, scores in fp64.
+// Out of line: the common path keeps its registers.
+__device__ __noinline__ void select_exactly(const SelectArgs& a, long t, WarpScratch& scratch) {
+    const int lane = threadIdx.x & 31;
     const float* row = a.logits + t * a.ld;
     float z[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         z[q] = lane + 32 * q < a.E ? cleaned(row[lane + 32 * q]) : -INFINITY;
-    float zmax = 0.f;
-    if (a.score_fn == MOE_SCORE_SOFTMAX) {
-        zmax = z[0];
-#pragma unroll
-        for (int q = 1; q < Q; ++q) zmax = fmaxf(zmax, z[q]);
-        zmax = warp_max_value(zmax);
-        if (zmax == -INFINITY) zmax = 0.f;  // every expert is out: all scores 0
-    }
+    const float zmax = a.score_fn == MOE_SCORE_SOFTMAX ? largest(z) : 0.f;
     int e = 0;
-    if (!choose<float>(a, z, zmax, scratch[warp].f, e)) {
-        __syncwarp();
-        choose<double>(a, z, zmax, scratch[warp].d, e);
-    }
-    // Lane j: the score of the j-th choice, and the weights. Where they are divided
-    // by their sum, a common factor is free: the softmax takes the largest chosen
-    // logit as its reference, and scores of logits so small that fp32 would lose
-    // them (sigmoid(z) = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are
-    // taken relative to the largest one's.
-    const float zj = lane < a.k ? cleaned(row[e]) : -INFINITY;
-    float s = 0.f;
-    if (a.renorm) {
-        const float zc = warp_max_value(zj);
-        if (a.score_fn == MOE_SCORE_SOFTMAX)
-            s = zc > -INFINITY ? expf(zj - zc) : 0.f;
-        else if (zc < -80.f)
-            s = zc > -INFINITY
-                    ? expf(a.score_fn == MOE_SCORE_SIGMOID ? zj - zc : 0.5f * (zj - zc)) : 0.f;
-        else
-            s = score_value(zj, a.score_fn);
-    } else {
-        s = a.score_fn == MOE_SCORE_SOFTMAX ? expf(zj - zmax) : score_value(zj, a.score_fn);
-    }
-    float den = 1.f;
-    if (a.renorm) {
-        den = warp_sum(s);
-    } else if (a.score_fn == MOE_SCORE_SOFTMAX) {
-        float part = 0.f;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) part += expf(z[q] - zmax);  // 0 for an expert that is out
-        den = warp_sum(part);
-    }
+    __syncwarp();
+    if (a.bias || (a.n_group > 1 && a.group_score == MOE_GROUP_TOP2))
+        choose<double>(a, z, zmax, scratch.d, e);
+    else
+        choose<float>(a, z, zmax, scratch.f, e);
+    __syncwarp();
+    const float w = weight_of(a, a.score_fn, z, zmax, lane < a.k ? cleaned(row[e]) : -INFINITY);
     if (lane < a.k) {
         a.idx[t * a.k + lane] = e;
-        a.w[t * a.k + lane] = den > 0.f ? a.scale * (s / den) : 0.f;
+        a.w[t * a.k + lane] = w;
     }
+}
+
+// Persistent warps, a token each in turn, the next token's logits on the way. The
+// packed choice is tried first; the tokens it leaves open (a bit each, of up to
+// 64) follow exactly. GROUPS: `lanes` (a power of two) lanes hold one group of n
+// experts, 8 a lane, so that a group's score is a few shuffles; otherwise lane l
+// holds the experts l, l + 32, ...
+template <int FN, bool GROUPS>
+__global__ void __launch_bounds__(WARPS * 32, kCtasPerSm)
+select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
+    pdl_launch_and_wait();
+    __shared__ WarpScratch scratch[WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = a.E / a.n_group;  // experts of a group
+    const int shift = __ffs(lanes) - 1;
+    const int group = lane >> shift, sub = lane & (lanes - 1);
+    auto expert = [&](int q) { return GROUPS ? group * n + sub * Q + q : lane + 32 * q; };
+    auto exists = [&](int q) {
+        return GROUPS ? group < a.n_group && sub * Q + q < n : lane + 32 * q < a.E;
+    };
+    const bool top2 = GROUPS && a.group_score == MOE_GROUP_TOP2;
+    const bool evaluated = a.bias || top2;  // scores take part in a comparison
+    float bias[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) bias[q] = a.bias && exists(q) ? cleaned(a.bias[expert(q)]) : 0.f;
+    const long step = (long)gridDim.x * WARPS;
+    float coming[Q];  // the next token's logits
+    auto load = [&](long t) {
+        const float* p = a.logits + t * a.ld + (GROUPS ? group * n + sub * Q : lane);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) coming[q] = exists(q) ? p[GROUPS ? q : 32 * q] : -INFINITY;
+    };
+    long t = (long)blockIdx.x * WARPS + warp;
+    if (t < a.T) load(t);
+    while (t < a.T) {
+        const long t0 = t;
+        unsigned long long open = 0;
+        for (int i = 0; i < 64 && t < a.T; ++i, t += step) {
+            float z[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) z[q] = cleaned(coming[q]);
+            if (t + step < a.T) load(t + step);
+            const float zmax = FN == MOE_SCORE_SOFTMAX ? largest(z) : 0.f;
+            // what experts are ranked by, and what groups sum
+            float c[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) c[q] = z[q];
+            if (evaluated) {
+                float inv = 1.f;
+                if (FN == MOE_SCORE_SOFTMAX) {
+                    float part = 0.f;
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) part += __expf(z[q] - zmax);
+                    inv = __fdividef(1.f, warp_sum(part));
+                }
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const float s = FN == MOE_SCORE_SOFTMAX ? __expf(z[q] - zmax) * inv
+                                                            : score_of(z[q], FN);
+                    c[q] = z[q] == -INFINITY ? -INFINITY : s + bias[q];
+                }
+            }
+            bool sure = true, kept = true;
+            if (GROUPS) {
+                float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    v2 = fmaxf(v2, fminf(v1, c[q]));
+                    v1 = fmaxf(v1, c[q]);
+                }
+                for (int o = 1; o < lanes; o <<= 1) {
+                    const float u1 = __shfl_xor_sync(0xffffffffu, v1, o);
+                    const float u2 = __shfl_xor_sync(0xffffffffu, v2, o);
+                    v2 = fmaxf(fmaxf(v2, u2), fminf(v1, u1));
+                    v1 = fmaxf(v1, u1);
+                }
+                const float own = top2 ? v1 + v2 : v1;
+                int ahead = 0;  // a group stays if fewer than topk_group are ahead of it
+                for (int g = 0; g < a.n_group; ++g) {
+                    const float v = __shfl_sync(0xffffffffu, own, g << shift);
+                    ahead += v > own || (v == own && g < group);
+                }
+                kept = ahead < a.topk_group;
+                if (evaluated && a.topk_group < a.n_group) {
+                    const uint32_t key = order_key(own);
+                    const bool is = group < a.n_group;
+                    sure = decided(
+                        key_value(__reduce_min_sync(0xffffffffu, kept && is ? key : ~0u)),
+                        key_value(__reduce_max_sync(0xffffffffu, kept || !is ? 0u : key)));
+                }
+            }
+            uint32_t h[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                h[q] = kept && exists(q)
+                           ? (order_key(top2 && !a.bias ? z[q] : c[q]) & ~7u) | (uint32_t)(7 - q)
+                           : 0u;
+            int e = 0;
+            if (!choose_packed(h, a.k, a.bias ? kScoreError : 0.f, e)) sure = false;
+            if (!sure) {
+                open |= 1ull << i;
+                continue;
+            }
+            const int l = e >> 3, q = e & 7;
+            e = GROUPS ? (l >> shift) * n + (l & (lanes - 1)) * Q + q : l + 32 * q;
+            const float* row = a.logits + t * a.ld;
+            const float w =
+                weight_of(a, FN, z, zmax, lane < a.k ? cleaned(row[e]) : -INFINITY);
+            if (lane < a.k) {
+                a.idx[t * a.k + lane] = e;
+                a.w[t * a.k + lane] = w;
+            }
+        }
+        while (open) {
+            const int i = __ffsll((long long)open) - 1;
+            open &= open - 1;
+            select_exactly(a, t0 + i * step, scratch[warp]);
+        }
+    }
+}
+
+// Groups that do not fit a warp's lanes (more than 32 / lanes of them).
+__global__ void __launch_bounds__(WARPS * 32, kCtasPerSm)
+select_exact_kernel(const __grid_constant__ SelectArgs a) {
+    pdl_launch_and_wait();
+    __shared__ WarpScratch scratch[WARPS];
+    const int warp = threadIdx.x >> 5;
+    for (long t = (long)blockIdx.x * WARPS + warp; t < a.T; t += (long)gridDim.x * WARPS)
+        select_exactly(a, t, scratch[warp]);
+}
+
+template <int FN>
+cudaError_t launch(const SelectArgs& a, cudaStream_t s) {
+    const long ctas = ((long)a.T + WARPS - 1) / WARPS, most = 148L * kCtasPerSm;
+    const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(WARPS * 32);
+    if (a.n_group == 1) return launch_pdl(select_kernel<FN, false>, grid, block, 0, s, a, 1);
+    int lanes = 1;
+    while (lanes * Q < a.E / a.n_group) lanes *= 2;
+    if (lanes * a.n_group <= 32)
+        return launch_pdl(select_kernel<FN, true>, grid, block, 0, s, a, lanes);
+    return launch_pdl(select_exact_kernel, grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -304,8 +470,10 @@ cudaError_t launch_select(const moe_config& c, const float* logits, long ld,
                           int32_t* idx, float* w, cudaStream_t s) {
     const SelectArgs a = {logits, ld, score_bias, score_fn, grp.n_group, grp.topk_group,
                           grp.group_score, grp.renormalize, c.T, c.E, c.k, c.scale, idx, w};
-    const cudaError_t err = launch_pdl(select_kernel, dim3((unsigned)((c.T + WARPS - 1) / WARPS)),
-                                       dim3(WARPS * 32), 0, s, a);
+    const cudaError_t err = score_fn == MOE_SCORE_SOFTMAX ? launch<MOE_SCORE_SOFTMAX>(a, s)
+                            : score_fn == MOE_SCORE_SQRT_SOFTPLUS
+                                ? launch<MOE_SCORE_SQRT_SOFTPLUS>(a, s)
+                                : launch<MOE_SCORE_SIGMOID>(a, s);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -192,13 +192,14 @@ def config(T: int, d: int, E: int, k: int, d_ff: int, scale: float = 2.826, fp8:
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _s(stream) -> ctypes.c_void_p:
+def _s(stream) -> int:
+    """The stream's handle (None: the current stream of the current device)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(fn: str, rc: int) -> None:
@@ -347,22 +348,26 @@ def moe_ep_row_experts(counts, n_src: int, e_local: int, expert_of_row, stream=N
 
 
 def _opt(o):
-    return None if o is None else ctypes.byref(o)
+    return o if o is None else ctypes.byref(o)
 
 
-def _rows(fn: str, t: torch.Tensor, cols: int) -> int:
-    """Row stride, in elements, of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+def _rows(fn: str, t: torch.Tensor, rows: int, cols: int) -> int:
+    """Row stride, in elements, of a [rows, cols] tensor whose rows are contiguous."""
+    if t.shape != (rows, cols):
         raise MoeError(fn, MOE_ERR_INVALID_ARG)
-    return t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0))
+    if t.is_contiguous():
+        return cols
+    if cols > 1 and t.stride(1) != 1:
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
-    if logits.dtype != torch.float32 or logits.shape[0] != cfg.T:
+    if logits.dtype != torch.float32:
         raise MoeError("moe_select", MOE_ERR_INVALID_ARG)
     _check("moe_select", lib().moe_select(ctypes.byref(cfg), _p(logits),
-                                          _rows("moe_select", logits, cfg.E), _opt(opt),
+                                          _rows("moe_select", logits, cfg.T, cfg.E), _opt(opt),
                                           _opt(grp), _p(topk_idx), _p(topk_w), _s(stream)))
 
 
@@ -393,12 +398,12 @@ def moe_block_quant(x, codes, scales, stream=None) -> None:
     """Quantise rows: x [M, K] bf16 (rows may be strided), codes [M, K] e4m3 (or uint8),
     scales [M, ceil(K/128)] fp32."""
     M, K = codes.shape
-    if x.dtype != torch.bfloat16 or x.shape != codes.shape or codes.element_size() != 1 or \
-            tuple(scales.shape) != (M, -(-K // 128)) or scales.dtype != torch.float32 or \
+    if x.dtype != torch.bfloat16 or scales.shape != (M, -(-K // 128)) or \
+            scales.dtype != torch.float32 or codes.element_size() != 1 or \
             not codes.is_contiguous() or not scales.is_contiguous():
         raise MoeError("moe_block_quant", MOE_ERR_INVALID_ARG)
     _check("moe_block_quant",
-           lib().moe_block_quant(_p(x), _rows("moe_block_quant", x, K), M, K, _p(codes),
+           lib().moe_block_quant(_p(x), _rows("moe_block_quant", x, M, K), M, K, _p(codes),
                                  _p(scales), _s(stream)))
 
 
@@ -419,9 +424,8 @@ def moe_block_gemm(xq, sx, wq, sw, out, ws, offsets=None, stream=None) -> None:
     M = xq.shape[0]
     kb, nb = -(-K // 128), -(-N // 128)
     lead = () if offsets is None else (G,)
-    if tuple(xq.shape) != (M, K) or tuple(sx.shape) != (M, kb) or \
-            tuple(wq.shape) != lead + (N, K) or tuple(sw.shape) != lead + (nb, kb) or \
-            tuple(out.shape) != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
+    if xq.shape != (M, K) or sx.shape != (M, kb) or wq.shape != lead + (N, K) or \
+            sw.shape != lead + (nb, kb) or out.shape != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
             (offsets is not None and (offsets.numel() != G + 1 or offsets.dtype != torch.int32)) or \
             xq.element_size() != 1 or wq.element_size() != 1 or sx.dtype != torch.float32 or \
             sw.dtype != torch.float32 or not all(t.is_contiguous() for t in (xq, sx, wq, sw, out)):
