@@ -16,7 +16,8 @@ namespace moe {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int CHUNK = 256;  // columns of a warp's pass: two blocks
+constexpr int CHUNK = 256;  // columns of a warp's load: two blocks
+constexpr int CTAS_PER_SM = 10;
 
 // The 8 columns [col, col + 8) of one row (u: their bf16 patterns; zero where
 // the row has ended) to 8 code bytes; the 16 lanes of the block share its scale.
@@ -28,81 +29,92 @@ __device__ __forceinline__ uint2 quantise8(const uint4& u, float& scale) {
     const uint32_t top = max(m >> 16, m & 0xFFFFu);
     const BlockScale b = block_scale(f32_from_bits(top << 16));
     scale = b.scale;
-    float f[8];
-    bf16x8_to_float(u, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = block_quotient(b, f[i]);
-    return make_uint2(e4m3x2_of(f[0], f[1]) | (e4m3x2_of(f[2], f[3]) << 16),
-                      e4m3x2_of(f[4], f[5]) | (e4m3x2_of(f[6], f[7]) << 16));
+    const BlockScale2 b2 = twice(b);
+    auto pair = [&](uint32_t v) {
+        const float2 x = bf16x2_to_float2(v);
+        const float2 q = block_quotient2(b2, x.x, x.y);
+        return e4m3x2_of(q.x, q.y);
+    };
+    return make_uint2(pair(u.x) | (pair(u.y) << 16), pair(u.z) | (pair(u.w) << 16));
 }
 
-// WPR warps share a row (a power of two <= WARPS), each taking every WPR-th
-// chunk. PERMUTE: row t goes to the kk rows row_of[t * kk + j] of the output
-// (entries outside [0, R) are skipped).
+// A unit is 256 columns of one row. The warps take the units in turn, U at a time
+// (2 KB on the way per warp), whatever the rows' length: row and chunk of a unit
+// follow from the last one's by an addition. PERMUTE: row t goes to the kk rows
+// row_of[t * kk + j] of the output (entries outside [0, R) are skipped).
 template <bool PERMUTE>
-__global__ void __launch_bounds__(WARPS * 32)
-block_quant_kernel(const __nv_bfloat16* __restrict__ x, long ldx, int M, int K, int wpr,
+__global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
+block_quant_kernel(const __nv_bfloat16* __restrict__ x, long ldx, int M, int K,
                    const int* __restrict__ row_of, int kk, long R, uint8_t* __restrict__ codes,
                    float* __restrict__ scales) {
     pdl_launch_and_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long row = (long)blockIdx.x * (WARPS / wpr) + warp / wpr;
-    if (row >= M) return;
-    const int kb = (K + 127) / 128;
-    const __nv_bfloat16* src = x + row * ldx;
-    constexpr int U = 4;  // chunks in flight
-    for (int c0 = (warp % wpr) * CHUNK; c0 < K; c0 += U * wpr * CHUNK) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31;
+    const int kb = (K + 127) / 128, chunks = (K + CHUNK - 1) / CHUNK;
+    const int warps = gridDim.x * WARPS, w = blockIdx.x * WARPS + (threadIdx.x >> 5);
+    const int d_row = warps / chunks, d_chunk = warps - d_row * chunks;
+    int row = w / chunks, chunk = w - row * chunks;
+    while (row < M) {
         uint4 u[U];
+        int r0[U], c0[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int col = c0 + i * wpr * CHUNK + lane * 8;
-            u[i] = col < K ? ld_stream_u4(src + col) : make_uint4(0, 0, 0, 0);
+            r0[i] = row;
+            c0[i] = chunk * CHUNK + lane * 8;
+            u[i] = row < M && c0[i] < K ? ld_stream_u4(x + row * ldx + c0[i])
+                                        : make_uint4(0, 0, 0, 0);
+            row += d_row;
+            chunk += d_chunk;
+            if (chunk >= chunks) {
+                chunk -= chunks;
+                ++row;
+            }
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int col = c0 + i * wpr * CHUNK + lane * 8;
+            if (r0[i] >= M) break;  // uniform
             float scale;
             const uint2 q = quantise8(u[i], scale);
-            if (col >= K) continue;
+            const int c = c0[i];
+            if (c >= K) continue;
             if constexpr (PERMUTE) {
                 for (int j = 0; j < kk; ++j) {
-                    const long r = row_of[row * kk + j];
+                    const long r = row_of[(long)r0[i] * kk + j];
                     if (r < 0 || r >= R) continue;
-                    *reinterpret_cast<uint2*>(codes + r * K + col) = q;
-                    if ((lane & 15) == 0) scales[r * kb + (col >> 7)] = scale;
+                    *reinterpret_cast<uint2*>(codes + r * K + c) = q;
+                    if ((lane & 15) == 0) scales[r * kb + (c >> 7)] = scale;
                 }
             } else {
-                *reinterpret_cast<uint2*>(codes + row * K + col) = q;
-                if ((lane & 15) == 0) scales[row * kb + (col >> 7)] = scale;
+                *reinterpret_cast<uint2*>(codes + (long)r0[i] * K + c) = q;
+                if ((lane & 15) == 0) scales[(long)r0[i] * kb + (c >> 7)] = scale;
             }
         }
     }
 }
 
-int warps_per_row(int K) {
-    const int chunks = (K + CHUNK - 1) / CHUNK;
-    return chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+unsigned grid_of(int M, int K) {
+    const long units = (long)M * ((K + CHUNK - 1) / CHUNK);
+    const long ctas = (units + WARPS - 1) / WARPS, most = 148L * CTAS_PER_SM;
+    return (unsigned)(ctas < most ? ctas : most);
 }
 
 }  // namespace
 
 cudaError_t launch_block_quant(const void* x, long ldx, int M, int K, void* codes, float* scales,
                                cudaStream_t s) {
-    const int wpr = warps_per_row(K), rows = WARPS / wpr;
-    const cudaError_t err =
-        launch_pdl(block_quant_kernel<false>, dim3((unsigned)((M + rows - 1) / rows)),
-                   dim3(WARPS * 32), 0, s, static_cast<const __nv_bfloat16*>(x), ldx, M, K, wpr,
-                   (const int*)nullptr, 1, 0L, static_cast<uint8_t*>(codes), scales);
+    const cudaError_t err = launch_pdl(
+        block_quant_kernel<false>, dim3(grid_of(M, K)), dim3(WARPS * 32), 0, s,
+        static_cast<const __nv_bfloat16*>(x), ldx, M, K, (const int*)nullptr, 1, 0L,
+        static_cast<uint8_t*>(codes), scales);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 cudaError_t launch_block_permute(const void* x, const int32_t* row_of, int T, int kk, int d,
                                  long R, void* codes, float* scales, cudaStream_t s) {
-    const int wpr = warps_per_row(d), rows = WARPS / wpr;
-    const cudaError_t err =
-        launch_pdl(block_quant_kernel<true>, dim3((unsigned)((T + rows - 1) / rows)),
-                   dim3(WARPS * 32), 0, s, static_cast<const __nv_bfloat16*>(x), (long)d, T, d, wpr,
-                   row_of, kk, R, static_cast<uint8_t*>(codes), scales);
+    const cudaError_t err = launch_pdl(
+        block_quant_kernel<true>, dim3(grid_of(T, d)), dim3(WARPS * 32), 0, s,
+        static_cast<const __nv_bfloat16*>(x), (long)d, T, d, row_of, kk, R,
+        static_cast<uint8_t*>(codes), scales);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
