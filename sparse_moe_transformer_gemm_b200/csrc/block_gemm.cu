@@ -5,10 +5,12 @@
 //   out[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{c in block b} xq[m, c] wq[n, c]
 //   gate_up:  h = SiLU(g) u in fp32, hq / sh its quantisation per 128 features
 //
-// Both kernels let the tensor core sum one block of 128 columns at a time into
-// TMEM and add it, scaled, to fp32 registers. They differ in what the MMA's 256
-// rows are: weight rows with up to 32 tokens as its columns (block_few.cu), or
-// tokens with 256 weight rows as its columns (block_many.cu).
+// The kernels let the tensor core sum one block of 128 columns at a time into TMEM
+// and add it, scaled, to fp32 registers. They differ in what the MMA's rows are:
+// weight rows with up to 32 tokens as its columns, on pairs of SMs (block_few.cu);
+// tokens with 256 weight rows as its columns, on pairs (block_many.cu); or weight
+// rows on single SMs that share the columns of K (block_split.cu), for one product
+// that is too small to give every pair a tile.
 #include "block_tile.cuh"
 
 namespace moe {
@@ -45,10 +47,22 @@ bool make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64_t cols) {
-    for (int lg = 0; lg < 4; ++lg)
+bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64_t cols,
+                          int boxes) {
+    for (int lg = 0; lg < boxes; ++lg)
         if (!make_byte_map(&tm->m[lg], base, rows, cols, NBOX << lg)) return false;
     return true;
+}
+
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return err;
 }
 
 int sm_pairs() {
@@ -69,6 +83,7 @@ bool few(const BlockGemm& p) { return (long)p.M <= kFewRows * p.G; }
 }  // namespace block
 
 cudaError_t launch_block_gemm(const BlockGemm& p, cudaStream_t s) {
+    if (block::splits(p)) return block::launch_split(p, s);
     return block::few(p) ? block::launch_few(p, false, s) : block::launch_many(p, false, s);
 }
 cudaError_t launch_block_gate_up(const BlockGemm& p, cudaStream_t s) {

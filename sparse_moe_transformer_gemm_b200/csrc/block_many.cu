@@ -438,6 +438,14 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     }
 }
 
+template <bool GATE_UP, bool OUT_F32>
+cudaError_t launch(const CUtensorMap& ma, const TokenMaps& mb, const Args& a, cudaStream_t s) {
+    static std::atomic<uint64_t> done{0};
+    auto kernel = block_many_kernel<GATE_UP, OUT_F32>;
+    const cudaError_t err = allow_smem((const void*)kernel, SMEM, done);
+    return err != cudaSuccess ? err : launch_pairs(kernel, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+}
+
 }  // namespace
 
 cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s) {
@@ -448,13 +456,13 @@ cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s) {
     CUtensorMap ma;
     TokenMaps mb;
     if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||
-        !make_token_byte_maps(&mb, p.xq, p.M, p.K))
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K, 4))
         return cudaErrorInvalidValue;
     if (gate_up)
-        return launch_pairs(block_many_kernel<true, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+        return launch<true, false>(ma, mb, a, s);
     if (p.out_type == MOE_OUT_F32)
-        return launch_pairs(block_many_kernel<false, true>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
-    return launch_pairs(block_many_kernel<false, false>, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+        return launch<false, true>(ma, mb, a, s);
+    return launch<false, false>(ma, mb, a, s);
 }
 
 }  // namespace block

@@ -4,6 +4,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "quant.cuh"
 #include "tc.cuh"
@@ -128,15 +130,17 @@ __device__ __forceinline__ float value_at(const uint64_t (&a)[N], int i) {
 // box_rows rows x 128 bytes, 128-byte swizzle.
 bool make_byte_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                    uint32_t box_rows);
-bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64_t cols);
+// make_token_byte_maps: the first `boxes` of them (16, 32, ... rows).
+bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64_t cols, int boxes);
 int sm_pairs();
 
+// A kernel's shared-memory limit, set once per device (`done`: a bit per device).
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done);
+
+// The kernel on `pairs` pairs of SMs (allow_smem comes first).
 template <typename Kernel>
 cudaError_t launch_pairs(Kernel kernel, int pairs, int threads, int smem, cudaStream_t s,
                          const CUtensorMap& ma, const TokenMaps& mb, const Args& a) {
-    cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(threads, 1, 1);
@@ -151,11 +155,14 @@ cudaError_t launch_pairs(Kernel kernel, int pairs, int threads, int smem, cudaSt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, a);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// The two kernels' launchers (block_few.cu, block_many.cu).
+// The kernels' launchers (block_split.cu, block_few.cu, block_many.cu); splits: K slices
+// of block_split's kernel, 0 where it does not take the product.
+int splits(const BlockGemm& p);
+cudaError_t launch_split(const BlockGemm& p, cudaStream_t s);
 cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s);
 cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s);
 
