@@ -51,6 +51,7 @@ struct Ctrl {
     uint32_t tmem_base;
     int abort;
     TileTable tab;
+    alignas(16) TileList list;
     alignas(16) float scales[SLOTS][COLS];
     alignas(16) uint32_t amax[2][CH][4];  // gate_up: a token's largest |h| per lane quarter
     alignas(16) float4 hscale[2][CH];     // gate_up: BlockScale of a token
@@ -122,6 +123,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     tc::fence_before_sync();
     tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc::fence_after_sync();
+    fill_list<NM>(c.list, c.tab, a.G, pair, n_pairs);
+    __syncthreads();
     const uint32_t tmem_base = tc::uniform(c.tmem_base);
     const int total = (int)tc::uniform(c.tab.total);
     const volatile int* abort_flag = &c.abort;
@@ -138,8 +141,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint64_t pol_x = tc::policy_evict_last();
         uint32_t it = 0;  // blocks loaded
         bool ok = true;
-        for (int t = pair; t < total && ok; t += n_pairs) {
-            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+        for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
             const bool second = two(ti.m);
             const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
             const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
@@ -177,8 +180,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, NM);
             uint32_t blk = 0;
             bool ok = true;
-            for (int t = pair; t < total && ok; t += n_pairs) {
-                const bool second = two((int)tc::uniform(tile_of<NM>(c.tab, a.G, t).m));
+            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                const bool second = two(listed_tile<NM>(c.list, c.tab, a.G, i_t, t).m);
                 for (int kb = 0; kb < KB; ++kb, ++blk) {
                     const uint32_t as = blk % ACC, stage = blk % STAGES;
                     if (!tc::mbar_wait_warp(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
@@ -219,8 +222,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
         uint32_t blk = 0;
         bool ok = true;
-        for (int t = pair; t < total && ok; t += n_pairs) {
-            const Tile ti = tile_of<NM>(c.tab, a.G, t);
+        for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
             const float* sxp = a.sx + (size_t)(ti.row0 + lane) * KB;
             const float* swp[2];
 #pragma unroll
@@ -266,8 +269,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0]), 0);
         uint8_t* tile = epi + grp * (EPI_BYTES / 2);
         uint32_t blk = 0;
-        for (int t = pair; t < total; t += n_pairs) {
-            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+        for (int t = pair, i_t = 0; t < total; t += n_pairs, ++i_t) {
+            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
             const int left = ti.len - grp * CH;  // valid tokens of this group
             const long tok0 = ti.row0 + grp * CH;
             const bool second = two(ti.m);

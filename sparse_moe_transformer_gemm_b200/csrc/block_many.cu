@@ -69,6 +69,7 @@ struct Ctrl {
     uint32_t tmem_base;
     int abort;
     TileTable tab;
+    alignas(16) TileList list;
     float amax[GROUPS][BM];   // gate_up: a token's largest |h| in each group's columns
     float factor[SLOTS][FB][2][BM];  // sx[token] * sw of the columns 0-127 and 128-255
 };
@@ -136,6 +137,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     tc::fence_before_sync();
     tc::cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
     tc::fence_after_sync();
+    fill_list<NM>(c.list, c.tab, a.G, pair, n_pairs);
+    __syncthreads();
     const uint32_t tmem_base = tc::uniform(c.tmem_base);
     const int total = (int)tc::uniform(c.tab.total);
     const volatile int* abort_flag = &c.abort;
@@ -155,8 +158,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         const uint32_t col1 = col0 + (GATE_UP ? 2 * CH : CH);
         const int nb_n = (a.N + 127) / 128;
         uint32_t blk = 0, batch = 0;
-        for (int t = pair; t < total; t += n_pairs) {
-            const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+        for (int t = pair, i_t = 0; t < total; t += n_pairs, ++i_t) {
+            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
             const int tok = rank * BM + row;                     // token within the tile
             const bool mine = tok < ti.len;
             const bool active = rank * BM + quad * 32 < ti.len;  // any token of the warp
@@ -216,6 +219,7 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 const BlockScale b = block_scale(f32_from_bits(
                     max(max(f32_bits(c.amax[0][row]), f32_bits(c.amax[1][row])),
                         max(f32_bits(c.amax[2][row]), f32_bits(c.amax[3][row])))));
+                const BlockScale2 b2 = twice(b);
                 if (mine) {
                     const long r = ti.row0 + tok;
                     if (grp == 0) a.out_scales[r * nb_n + ti.m] = b.scale;
@@ -228,11 +232,11 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         for (int v = 0; v < 4; ++v) {
                             const int j = q * 16 + v * 4;
                             const auto& h = acc[0];
-                            w[v] = e4m3x2_of(block_quotient(b, value_at(h, j)),
-                                             block_quotient(b, value_at(h, j + 1))) |
-                                   (e4m3x2_of(block_quotient(b, value_at(h, j + 2)),
-                                              block_quotient(b, value_at(h, j + 3)))
-                                    << 16);
+                            const float2 q0 =
+                                block_quotient2(b2, value_at(h, j), value_at(h, j + 1));
+                            const float2 q1 =
+                                block_quotient2(b2, value_at(h, j + 2), value_at(h, j + 3));
+                            w[v] = e4m3x2_of(q0.x, q0.y) | (e4m3x2_of(q1.x, q1.y) << 16);
                         }
                         o[q] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
@@ -302,8 +306,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             const uint64_t pol_x = tc::policy_evict_last();
             uint32_t it = 0;  // blocks loaded
             bool ok = true;
-            for (int t = pair; t < total && ok; t += n_pairs) {
-                const Tile ti = uniform_tile(tile_of<NM>(c.tab, a.G, t));
+            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
                 // the rows that exist, in 16-row boxes (what the rest of the stage
                 // holds only reaches TMEM lanes that nobody reads)
                 const int r0 = (min(ti.len, BM) + 15) & ~15;
@@ -385,8 +389,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
             uint32_t batch = 0;
             bool ok = true;
-            for (int t = pair; t < total && ok; t += n_pairs) {
-                const Tile ti = tile_of<NM>(c.tab, a.G, t);
+            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
                 const float* sxp = a.sx + (size_t)(ti.row0 + rank * BM + lane) * KB;
                 const int left = ti.len - rank * BM - lane;
                 const int nb0 = GATE_UP ? ti.m : ti.m * 2;

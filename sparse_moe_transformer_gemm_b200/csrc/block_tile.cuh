@@ -94,10 +94,36 @@ __device__ __forceinline__ Tile tile_of(const TileTable& c, int G, int t) {
     return Tile{lo, m, c.off[lo] + j * NM, min(NM, rows - j * NM)};
 }
 
+// A pair's tiles pair, pair + n_pairs, ..., looked up once by the whole block (each
+// role would spend 300 to 1000 cycles a tile on it); the ones past the list's end
+// are looked up as they come.
+constexpr int LIST = 256;
+struct TileList {
+    int4 t[LIST];
+};
+template <int NM>
+__device__ __forceinline__ void fill_list(TileList& l, const TileTable& c, int G, int pair,
+                                          int n_pairs) {
+    for (int i = threadIdx.x; i < LIST; i += blockDim.x) {
+        const int t = pair + i * n_pairs;
+        if (t >= c.total) break;
+        const Tile ti = tile_of<NM>(c, G, t);
+        l.t[i] = make_int4(ti.g, ti.m, ti.row0, ti.len);
+    }
+}
+
 // The tile in uniform registers (all lanes hold the same one).
 __device__ __forceinline__ Tile uniform_tile(const Tile& t) {
     return Tile{(int)tc::uniform(t.g), (int)tc::uniform(t.m), (int)tc::uniform(t.row0),
                 (int)tc::uniform(t.len)};
+}
+
+template <int NM>
+__device__ __forceinline__ Tile listed_tile(const TileList& l, const TileTable& c, int G, int i,
+                                            int t) {
+    if (i >= LIST) return uniform_tile(tile_of<NM>(c, G, t));
+    const int4 v = l.t[i];
+    return uniform_tile(Tile{v.x, v.y, v.z, v.w});
 }
 
 // `rows` (a multiple of 16, at most 128) token rows from `row` on, as at most

@@ -95,13 +95,22 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 }
 
 // The same for waits that a pipeline's step depends on: the wall clock is read
-// (which takes as long as several hand-offs) only after `POLLS` tries.
-template <int POLLS = 4096>
+// (which takes as long as several hand-offs) only once in 1024 tries, and the
+// loop is one rolled one (the compiler unrolls a counted loop of tries; a kernel
+// whose roles' loops do not fit the instruction cache together loses a factor of
+// two).
 __device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
                                               const volatile int* abort_flag) {
-    for (int i = 0; i < POLLS; ++i)
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_for(bar, parity, abort_flag, kWaitNs);
+        if ((i & 1023u) == 0u) {
+            const uint64_t now = globaltimer_ns();
+            if (*abort_flag || (t0 && now - t0 > kWaitNs)) return false;
+            if (!t0) t0 = now;
+        }
+    }
 }
 
 // mbar_wait_hot by a converged warp: all lanes get the same answer.
