@@ -29,22 +29,32 @@ namespace {
 
 constexpr int BM = 128;                // weight rows per CTA and accumulator
 constexpr int A_BYTES = BM * BK;
-constexpr int NM = 32;                 // tokens per pair tile
-constexpr int CH = NM / 2;             // tokens per promotion group, and staged per CTA
-constexpr int STAGE_BYTES = 2 * A_BYTES + CH * BK;
-constexpr int STAGES = 6;
-constexpr int COLS = 2 * NM;           // TMEM columns per block
-constexpr int ACC = 512 / COLS;        // blocks in flight
+constexpr int CH = 16;                 // tokens per promotion chunk
 constexpr int SLOTS = 8;               // factor ring
 constexpr int SCALE_WARP = 2, PROMO_WARP = 4;
 constexpr int THREADS = 32 * (PROMO_WARP + 8);
-constexpr int EPI_BYTES = 2 * CH * BM * 2;  // a [16 tokens][128 rows] bf16 tile per group
+// up to so many rows a group on average, tiles of 32 tokens
+constexpr long kFewRows32 = 20;
 
+// NM: tokens per pair tile at most.
+template <int NM>
+struct Shape {
+    static constexpr int STAGE_BYTES = 2 * A_BYTES + NM / 2 * BK;  // 34 / 36 / 40 KB
+    static constexpr int STAGES = NM == 32 ? 6 : 5;
+    static constexpr int COLS = 2 * NM;     // TMEM columns per block
+    static constexpr int ACC = 512 / COLS;  // blocks in flight
+    static constexpr int NCH = NM / 2 / CH; // chunks of a group and accumulator
+    // per group: gate_up a [NM / 2 tokens][128 features] tile of codes, else a [16
+    // tokens][128 rows] tile of bf16
+    static constexpr int EPI_BYTES = 2 * (NM / 2 * BM > CH * BM * 2 ? NM / 2 * BM : CH * BM * 2);
+};
+
+template <int NM>
 struct Ctrl {
-    uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
-    uint64_t empty[STAGES];   // both CTAs: the pair MMAs finished reading the stage
-    uint64_t acc_full[ACC];   // both CTAs: a block's sums are in TMEM
-    uint64_t acc_empty[ACC];  // even CTA: every promotion warp of both CTAs has read them
+    uint64_t full[Shape<NM>::STAGES];    // even CTA: TMA bytes of both CTAs landed
+    uint64_t empty[Shape<NM>::STAGES];   // both CTAs: the pair MMAs finished reading the stage
+    uint64_t acc_full[Shape<NM>::ACC];   // both CTAs: a block's sums are in TMEM
+    uint64_t acc_empty[Shape<NM>::ACC];  // even CTA: every promotion warp has read them
     uint64_t sc_full[SLOTS];
     uint64_t sc_empty[SLOTS];
     uint64_t drain;
@@ -52,14 +62,18 @@ struct Ctrl {
     int abort;
     TileTable tab;
     alignas(16) TileList list;
-    alignas(16) float scales[SLOTS][COLS];
-    alignas(16) uint32_t amax[2][CH][4];  // gate_up: a token's largest |h| per lane quarter
-    alignas(16) float4 hscale[2][CH];     // gate_up: BlockScale of a token
+    alignas(16) float scales[SLOTS][Shape<NM>::COLS];
+    alignas(16) float4 hscale[2][NM / 2];  // gate_up: BlockScale of a token
 };
-constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + (int)sizeof(Ctrl);
-static_assert(SMEM <= 232448, "fits in 227 KB");
+template <int NM>
+constexpr int smem_bytes() {
+    return Shape<NM>::STAGES * Shape<NM>::STAGE_BYTES + Shape<NM>::EPI_BYTES + 1024 +
+           (int)sizeof(Ctrl<NM>);
+}
+static_assert(smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448, "fits in 227 KB");
 
-__device__ __forceinline__ void give_up(Ctrl& c, int* status) {
+template <int NM>
+__device__ __forceinline__ void give_up(Ctrl<NM>& c, int* status) {
     *reinterpret_cast<volatile int*>(&c.abort) = 1;
     atomicExch(status, MOE_ERR_TIMEOUT);
 }
@@ -76,15 +90,17 @@ __device__ __forceinline__ void promote(uint64_t (&acc)[CH / 2], const uint32_t 
 }
 
 // tmA: weights [G * w_rows, K] bytes, box 128 x 128; tmB: tokens [M, K] bytes.
-template <bool GATE_UP, bool OUT_F32>
+template <bool GATE_UP, bool OUT_F32, int NM>
 __global__ void __launch_bounds__(THREADS, 1)
 block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ TokenMaps tmB,
                  const Args a) {
+    using S = Shape<NM>;
+    constexpr int STAGES = S::STAGES, ACC = S::ACC, COLS = S::COLS, NCH = S::NCH;
     pdl_launch_and_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // stays a shared pointer
-    uint8_t* epi = smem + STAGES * STAGE_BYTES;
-    Ctrl& c = *reinterpret_cast<Ctrl*>(epi + EPI_BYTES);
+    uint8_t* epi = smem + STAGES * S::STAGE_BYTES;
+    Ctrl<NM>& c = *reinterpret_cast<Ctrl<NM>*>(epi + S::EPI_BYTES);
     const int warp = (int)tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int rank = (int)(tc::cluster_ctarank() & 1u);
     const bool leader = rank == 0;
@@ -97,7 +113,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (lane == 0) {
             c.abort = 0;
             tc::prefetch_tensormap(&tmA);
-            tc::prefetch_tensormap(&tmB.m[0]);
+            for (int m = 0; m < (NM == 32 ? 1 : 2); ++m) tc::prefetch_tensormap(&tmB.m[m]);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -132,11 +148,13 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     auto first_row = [&](int m, int p) {
         return GATE_UP ? p * a.N + m * 2 * BM + rank * BM : m * 4 * BM + p * 2 * BM + rank * BM;
     };
+    // the MMA's N: 32, or the tile's tokens rounded up to 32
+    auto tokens_of = [&](const Tile& ti) { return NM == 32 ? 32 : (ti.len + 31) & ~31; };
     // whether the pair's accumulator 1 has rows (always in gate_up)
     auto two = [&](int m) { return GATE_UP || m * 4 * BM + 2 * BM < a.N; };
 
     if (warp == 0) {
-        // ---------------- producer: this CTA's weight rows and 16 tokens
+        // ---------------- producer: this CTA's weight rows and half of the tokens
         const uint64_t pol_w = tc::policy_evict_first();
         const uint64_t pol_x = tc::policy_evict_last();
         uint32_t it = 0;  // blocks loaded
@@ -146,7 +164,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             const bool second = two(ti.m);
             const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
             const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
-            const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + CH * BK);
+            const int half = tokens_of(ti) / 2;
+            const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + half * BK);
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 const uint32_t stage = it % STAGES;
                 if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u, abort_flag)) {
@@ -155,13 +174,17 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     break;
                 }
                 const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
-                uint8_t* s = smem + stage * STAGE_BYTES;
+                uint8_t* s = smem + stage * S::STAGE_BYTES;
                 if (tc::elect_one()) {
                     if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
                     tc::tma_load_2d_pair(s, &tmA, bar, kb * BK, w0, pol_w);
                     if (second) tc::tma_load_2d_pair(s + A_BYTES, &tmA, bar, kb * BK, w1, pol_w);
-                    tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
-                                         ti.row0 + rank * CH, pol_x);
+                    if (NM == 32)
+                        tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
+                                             ti.row0 + rank * CH, pol_x);
+                    else
+                        load_tokens(s + 2 * A_BYTES, tmB, bar, kb * BK, ti.row0 + rank * half,
+                                    half, pol_x);
                 }
                 __syncwarp();
             }
@@ -176,12 +199,13 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp == 1) {
         if (leader) {
-            // ---------------- MMA issuer (even CTA): 256 weight rows x 32 tokens, twice
-            const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, NM);
+            // ---------------- MMA issuer (even CTA): 256 weight rows x n tokens, twice
             uint32_t blk = 0;
             bool ok = true;
             for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
-                const bool second = two(listed_tile<NM>(c.list, c.tab, a.G, i_t, t).m);
+                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
+                const bool second = two(ti.m);
+                const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, tokens_of(ti));
                 for (int kb = 0; kb < KB; ++kb, ++blk) {
                     const uint32_t as = blk % ACC, stage = blk % STAGES;
                     if (!tc::mbar_wait_warp(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
@@ -192,7 +216,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     }
                     tc::fence_after_sync();
                     const uint32_t d = tmem_base + as * COLS;
-                    const uint32_t w = tc::smem_u32(smem + stage * STAGE_BYTES);
+                    const uint32_t w = tc::smem_u32(smem + stage * S::STAGE_BYTES);
                     if (tc::elect_one()) {
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k) {
@@ -214,10 +238,10 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
         }
     } else if (warp == SCALE_WARP) {
-        // ---------------- factors: per block sx[token] * sw of this CTA's weight rows,
-        // lane = token, 4 blocks loaded at a time. The ring runs ahead of the
-        // promotion, over tile borders too.
-        constexpr int U = 4;
+        // ---------------- factors: per block sx[token] * sw of this CTA's weight rows, U
+        // blocks loaded at a time. The ring runs ahead of the promotion, over tile
+        // borders too.
+        constexpr int U = 4, TPL = NM / 32;  // tokens per lane
         const int nb_n = (a.N + 127) / 128;
         const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
         uint32_t blk = 0;
@@ -232,26 +256,31 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 swp[p] = a.sw + ((size_t)ti.g * sw_rows + nb) * KB;
             }
             for (int k0 = 0; k0 < KB && ok; k0 += U) {
-                float x[U], w[2][U];
+                float x[TPL][U], w[2][U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const bool in = k0 + u < KB;
                     w[0][u] = in ? swp[0][k0 + u] : 0.f;
                     w[1][u] = in ? swp[1][k0 + u] : 0.f;
-                    x[u] = in && lane < ti.len ? sxp[k0 + u] : 0.f;
+#pragma unroll
+                    for (int i = 0; i < TPL; ++i)
+                        x[i][u] = in && lane + 32 * i < ti.len
+                                      ? sxp[(size_t)(32 * i) * KB + k0 + u] : 0.f;
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (k0 + u >= KB || !ok) continue;
                     const uint32_t slot = blk % SLOTS;
-                    ok = tc::mbar_wait_hot(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u, abort_flag);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = tc::mbar_wait_warp(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u, abort_flag);
                     if (!ok) {
                         give_up(c, a.status);
                         continue;
                     }
-                    c.scales[slot][lane] = x[u] * w[0][u];
-                    c.scales[slot][NM + lane] = x[u] * w[1][u];
+#pragma unroll
+                    for (int i = 0; i < TPL; ++i) {
+                        c.scales[slot][lane + 32 * i] = x[i][u] * w[0][u];
+                        c.scales[slot][NM + lane + 32 * i] = x[i][u] * w[1][u];
+                    }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
                     ++blk;
@@ -260,46 +289,56 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         }
     } else if (warp >= PROMO_WARP) {
         // ---------------- promotion and epilogue: lane = one weight row of each
-        // accumulator; group grp takes the tokens [16 grp, 16 grp + 16)
+        // accumulator; group grp takes the tokens [grp * half, (grp + 1) * half), half of
+        // the MMA's N, in chunks of 16
         const int quad = warp & 3, grp = (warp - PROMO_WARP) >> 2;
         const int et = threadIdx.x - 32 * PROMO_WARP - 128 * grp;  // 0..127 within the group
         const int bar = 1 + grp;
         const int row = quad * 32 + lane;                          // of the CTA's 128
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16) + grp * CH;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
         const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0]), 0);
-        uint8_t* tile = epi + grp * (EPI_BYTES / 2);
+        uint8_t* tile = epi + grp * (S::EPI_BYTES / 2);
         uint32_t blk = 0;
         for (int t = pair, i_t = 0; t < total; t += n_pairs, ++i_t) {
             const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-            const int left = ti.len - grp * CH;  // valid tokens of this group
-            const long tok0 = ti.row0 + grp * CH;
+            const int half = tokens_of(ti) / 2, col0 = grp * half;
+            const int left = min(half, ti.len - col0);  // valid tokens of this group
+            const long tok0 = ti.row0 + col0;
             const bool second = two(ti.m);
-            uint64_t acc[2][CH / 2];
+            uint64_t acc[2][NCH][CH / 2];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int j = 0; j < CH / 2; ++j) acc[p][j] = 0;
+                for (int i = 0; i < NCH; ++i)
+#pragma unroll
+                    for (int j = 0; j < CH / 2; ++j) acc[p][i][j] = 0;
             bool ok = true;
             for (int kb = 0; kb < KB; ++kb, ++blk) {
                 const uint32_t as = blk % ACC, slot = blk % SLOTS;
-                ok = tc::mbar_wait_hot(&c.sc_full[slot], (blk / SLOTS) & 1u, abort_flag) &&
-                     tc::mbar_wait_hot(&c.acc_full[as], (blk / ACC) & 1u, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);  // the warp stays together
+                ok = tc::mbar_wait_warp(&c.sc_full[slot], (blk / SLOTS) & 1u, abort_flag) &&
+                     tc::mbar_wait_warp(&c.acc_full[as], (blk / ACC) & 1u, abort_flag);
                 if (!ok) break;
                 if (left > 0) {
                     tc::fence_after_sync();
-                    const uint32_t tb = lane_base + as * COLS;
-                    uint32_t d0[CH], d1[CH];
-                    tc::tmem_ld16(tb, d0);
-                    if (second) tc::tmem_ld16(tb + NM, d1);
-                    tc::tmem_ld_wait();
-                    tc::tmem_loaded(d0);
-                    if (second) tc::tmem_loaded(d1);
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
-                    promote(acc[0], d0, c.scales[slot] + grp * CH);
-                    if (second) promote(acc[1], d1, c.scales[slot] + NM + grp * CH);
+                    const uint32_t tb = lane_base + as * COLS + col0;
+                    const float* sc = c.scales[slot] + col0;
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) {
+                        if (i * CH >= left) continue;
+                        uint32_t d0[CH], d1[CH];
+                        tc::tmem_ld16(tb + i * CH, d0);
+                        if (second) tc::tmem_ld16(tb + NM + i * CH, d1);
+                        tc::tmem_ld_wait();
+                        tc::tmem_loaded(d0);
+                        if (second) tc::tmem_loaded(d1);
+                        if ((i + 1) * CH >= left) {  // the last chunk: the block is read
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
+                        }
+                        promote(acc[0][i], d0, sc + i * CH);
+                        if (second) promote(acc[1][i], d1, sc + NM + i * CH);
+                    }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&c.sc_empty[slot]);
                 } else if (lane == 0) {
@@ -315,42 +354,56 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             if (left <= 0) continue;
             if constexpr (GATE_UP) {
                 const int f0 = ti.m * 2 * BM + rank * BM;  // first feature of the CTA's block
-                uint32_t mx = 0;
+                // a token's largest |h| of each lane quarter, in the tile's space
+                uint32_t (*amax)[4] = reinterpret_cast<uint32_t(*)[4]>(tile);
 #pragma unroll
-                for (int j = 0; j < CH; j += 2) {
-                    const float h0 = silu_mul(value_at(acc[0], j), value_at(acc[1], j));
-                    const float h1 = silu_mul(value_at(acc[0], j + 1), value_at(acc[1], j + 1));
-                    acc[0][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
-                    const uint32_t m0 = __reduce_max_sync(0xffffffffu, f32_bits(h0) & 0x7FFFFFFFu);
-                    const uint32_t m1 = __reduce_max_sync(0xffffffffu, f32_bits(h1) & 0x7FFFFFFFu);
-                    if (lane == j) mx = m0;
-                    if (lane == j + 1) mx = m1;
+                for (int i = 0; i < NCH; ++i) {
+                    if (i * CH >= left) continue;
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int j = 0; j < CH; j += 2) {
+                        const float h0 = silu_mul(value_at(acc[0][i], j), value_at(acc[1][i], j));
+                        const float h1 =
+                            silu_mul(value_at(acc[0][i], j + 1), value_at(acc[1][i], j + 1));
+                        acc[0][i][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
+                        const uint32_t m0 =
+                            __reduce_max_sync(0xffffffffu, f32_bits(h0) & 0x7FFFFFFFu);
+                        const uint32_t m1 =
+                            __reduce_max_sync(0xffffffffu, f32_bits(h1) & 0x7FFFFFFFu);
+                        if (lane == j) mx = m0;
+                        if (lane == j + 1) mx = m1;
+                    }
+                    if (lane < CH) amax[i * CH + lane][quad] = mx;
                 }
-                if (lane < CH) c.amax[grp][lane][quad] = mx;
                 tc::bar_sync(bar, 128);
-                if (et < CH) {
-                    const uint4 m = *reinterpret_cast<const uint4*>(c.amax[grp][et]);
+                if (et < left) {
+                    const uint4 m = *reinterpret_cast<const uint4*>(amax[et]);
                     const BlockScale b =
                         block_scale(f32_from_bits(max(max(m.x, m.y), max(m.z, m.w))));
                     c.hscale[grp][et] = make_float4(b.a, b.inv, b.move, b.scale);
-                    if (et < left && f0 < a.N)
-                        a.out_scales[(tok0 + et) * (a.N / 128) + (f0 >> 7)] = b.scale;
+                    if (f0 < a.N) a.out_scales[(tok0 + et) * (a.N / 128) + (f0 >> 7)] = b.scale;
                 }
                 tc::bar_sync(bar, 128);
-                // codes through a [16 tokens][128 features] tile to 16-byte stores
+                // codes through a [tokens][128 features] tile to 16-byte stores
 #pragma unroll
-                for (int j = 0; j < CH; ++j) {
-                    const float4 v = c.hscale[grp][j];
-                    const BlockScale b = {v.w, v.x, v.y, v.z};
-                    tile[j * BM + row] =
-                        (uint8_t)e4m3x2_of(block_quotient(b, value_at(acc[0], j)), 0.f);
+                for (int i = 0; i < NCH; ++i) {
+                    if (i * CH >= left) continue;
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) {
+                        const float4 v = c.hscale[grp][i * CH + j];
+                        const BlockScale b = {v.w, v.x, v.y, v.z};
+                        tile[(i * CH + j) * BM + row] =
+                            (uint8_t)e4m3x2_of(block_quotient(b, value_at(acc[0][i], j)), 0.f);
+                    }
                 }
                 tc::bar_sync(bar, 128);
-                const int n = et / (BM / 16), ch = et % (BM / 16);
-                if (f0 < a.N && n < left)
-                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (tok0 + n) * a.N + f0 +
-                                              ch * 16) =
-                        *reinterpret_cast<const uint4*>(tile + n * BM + ch * 16);
+                if (f0 < a.N)
+                    for (int id = et; id < left * (BM / 16); id += 128) {
+                        const int n = id / (BM / 16), ch = id % (BM / 16);
+                        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (tok0 + n) * a.N +
+                                                  f0 + ch * 16) =
+                            *reinterpret_cast<const uint4*>(tile + n * BM + ch * 16);
+                    }
                 // (the next tile's bar_any comes before the next writes here)
             } else {
                 const bool vec = !OUT_F32 && a.N % 8 == 0;
@@ -359,33 +412,38 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 for (int p = 0; p < 2; ++p) {
                     const int n0 = first_row(ti.m, p);  // first output column
                     if (p == 1 && !second) continue;
-                    if (vec) {
-                        // through a [16 tokens][128 rows] tile to 16-byte stores
-                        if (p == 1) tc::bar_sync(bar, 128);  // the first half is read
 #pragma unroll
-                        for (int j = 0; j < CH; ++j)
-                            o[j * BM + row] = float_to_bf16_bits(value_at(acc[p], j));
-                        tc::bar_sync(bar, 128);
+                    for (int i = 0; i < NCH; ++i) {
+                        if (i * CH >= left) continue;
+                        if (vec) {
+                            // through a [16 tokens][128 rows] tile to 16-byte stores
+                            if (p + i > 0) tc::bar_sync(bar, 128);  // the last one is read
 #pragma unroll
-                        for (int q = 0; q < CH * BM / 8 / 128; ++q) {
-                            const int id = et + 128 * q;
-                            const int n = id / (BM / 8), ch = id % (BM / 8);
-                            if (n < left && n0 + ch * 8 < a.N)
-                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                                          (tok0 + n) * a.N + n0 + ch * 8) =
-                                    *reinterpret_cast<const uint4*>(o + n * BM + ch * 8);
-                        }
-                    } else if (n0 + row < a.N) {
+                            for (int j = 0; j < CH; ++j)
+                                o[j * BM + row] = float_to_bf16_bits(value_at(acc[p][i], j));
+                            tc::bar_sync(bar, 128);
 #pragma unroll
-                        for (int j = 0; j < CH; ++j)
-                            if (j < left) {
-                                const long at = (tok0 + j) * a.N + n0 + row;
-                                if (OUT_F32)
-                                    static_cast<float*>(a.out)[at] = value_at(acc[p], j);
-                                else
-                                    static_cast<uint16_t*>(a.out)[at] =
-                                        float_to_bf16_bits(value_at(acc[p], j));
+                            for (int q = 0; q < CH * BM / 8 / 128; ++q) {
+                                const int id = et + 128 * q;
+                                const int n = id / (BM / 8), ch = id % (BM / 8);
+                                if (i * CH + n < left && n0 + ch * 8 < a.N)
+                                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                                              (tok0 + i * CH + n) * a.N + n0 +
+                                                              ch * 8) =
+                                        *reinterpret_cast<const uint4*>(o + n * BM + ch * 8);
                             }
+                        } else if (n0 + row < a.N) {
+#pragma unroll
+                            for (int j = 0; j < CH; ++j)
+                                if (i * CH + j < left) {
+                                    const long at = (tok0 + i * CH + j) * a.N + n0 + row;
+                                    if (OUT_F32)
+                                        static_cast<float*>(a.out)[at] = value_at(acc[p][i], j);
+                                    else
+                                        static_cast<uint16_t*>(a.out)[at] =
+                                            float_to_bf16_bits(value_at(acc[p][i], j));
+                                }
+                        }
                     }
                 }
             }
@@ -403,17 +461,18 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
 }
 
-template <bool GATE_UP, bool OUT_F32>
+template <bool GATE_UP, bool OUT_F32, int NM>
 cudaError_t launch(const CUtensorMap& ma, const TokenMaps& mb, const Args& a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    auto kernel = block_few_kernel<GATE_UP, OUT_F32>;
-    const cudaError_t err = allow_smem((const void*)kernel, SMEM, done);
-    return err != cudaSuccess ? err : launch_pairs(kernel, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
+    auto kernel = block_few_kernel<GATE_UP, OUT_F32, NM>;
+    const cudaError_t err = allow_smem((const void*)kernel, smem_bytes<NM>(), done);
+    return err != cudaSuccess
+               ? err
+               : launch_pairs(kernel, sm_pairs(), THREADS, smem_bytes<NM>(), s, ma, mb, a);
 }
 
-}  // namespace
-
-cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
+template <int NM>
+cudaError_t launch_nm(const BlockGemm& p, bool gate_up, cudaStream_t s) {
     const int w_rows = gate_up ? 2 * p.N : p.N;
     const int per_tile = gate_up ? 2 * BM : 4 * BM;
     const Args a = {p.sx, p.sw, p.offsets, p.G, p.M, p.N, p.K, (p.N + per_tile - 1) / per_tile,
@@ -421,13 +480,18 @@ cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
     CUtensorMap ma;
     TokenMaps mb;
     if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||
-        !make_token_byte_maps(&mb, p.xq, p.M, p.K, 1))
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K, NM == 32 ? 1 : 2))
         return cudaErrorInvalidValue;
-    if (gate_up)
-        return launch<true, false>(ma, mb, a, s);
-    if (p.out_type == MOE_OUT_F32)
-        return launch<false, true>(ma, mb, a, s);
-    return launch<false, false>(ma, mb, a, s);
+    if (gate_up) return launch<true, false, NM>(ma, mb, a, s);
+    if (p.out_type == MOE_OUT_F32) return launch<false, true, NM>(ma, mb, a, s);
+    return launch<false, false, NM>(ma, mb, a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
+    return (long)p.M <= kFewRows32 * p.G ? launch_nm<32>(p, gate_up, s)
+                                         : launch_nm<64>(p, gate_up, s);
 }
 
 }  // namespace block
