@@ -33,14 +33,18 @@ constexpr int CH = 16;                 // tokens per promotion chunk
 constexpr int SLOTS = 8;               // factor ring
 constexpr int SCALE_WARP = 2, PROMO_WARP = 4;
 constexpr int THREADS = 32 * (PROMO_WARP + 8);
-// up to so many rows a group on average, tiles of 32 tokens
-constexpr long kFewRows32 = 20;
+// Registers a thread with tiles of 128 tokens, whose promotion holds 128
+// accumulators: 168 at launch; 3 * 168 = 72 + 2 * 216.
+constexpr int REGS_FEW = 72, REGS_MANY = 216;
+static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
+// up to so many rows a group on average, tiles of 32 and of 64 tokens
+constexpr long kFewRows32 = 20, kFewRows64 = 56;
 
 // NM: tokens per pair tile at most.
 template <int NM>
 struct Shape {
     static constexpr int STAGE_BYTES = 2 * A_BYTES + NM / 2 * BK;  // 34 / 36 / 40 KB
-    static constexpr int STAGES = NM == 32 ? 6 : 5;
+    static constexpr int STAGES = NM == 32 ? 6 : NM == 64 ? 5 : 4;
     static constexpr int COLS = 2 * NM;     // TMEM columns per block
     static constexpr int ACC = 512 / COLS;  // blocks in flight
     static constexpr int NCH = NM / 2 / CH; // chunks of a group and accumulator
@@ -48,6 +52,8 @@ struct Shape {
     // tokens][128 rows] tile of bf16
     static constexpr int EPI_BYTES = 2 * (NM / 2 * BM > CH * BM * 2 ? NM / 2 * BM : CH * BM * 2);
 };
+
+constexpr int boxes(int NM) { return NM == 32 ? 1 : NM == 64 ? 2 : 3; }  // token maps in use
 
 template <int NM>
 struct Ctrl {
@@ -70,7 +76,8 @@ constexpr int smem_bytes() {
     return Shape<NM>::STAGES * Shape<NM>::STAGE_BYTES + Shape<NM>::EPI_BYTES + 1024 +
            (int)sizeof(Ctrl<NM>);
 }
-static_assert(smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448, "fits in 227 KB");
+static_assert(smem_bytes<32>() <= 232448 && smem_bytes<64>() <= 232448 &&
+                  smem_bytes<128>() <= 232448, "fits in 227 KB");
 
 template <int NM>
 __device__ __forceinline__ void give_up(Ctrl<NM>& c, int* status) {
@@ -96,6 +103,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                  const Args a) {
     using S = Shape<NM>;
     constexpr int STAGES = S::STAGES, ACC = S::ACC, COLS = S::COLS, NCH = S::NCH;
+    constexpr int R = NCH >= 2 ? 2 : 1;  // chunks per load round
     pdl_launch_and_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);  // stays a shared pointer
@@ -113,7 +121,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         if (lane == 0) {
             c.abort = 0;
             tc::prefetch_tensormap(&tmA);
-            for (int m = 0; m < (NM == 32 ? 1 : 2); ++m) tc::prefetch_tensormap(&tmB.m[m]);
+            for (int m = 0; m < boxes(NM); ++m) tc::prefetch_tensormap(&tmB.m[m]);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -153,141 +161,8 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     // whether the pair's accumulator 1 has rows (always in gate_up)
     auto two = [&](int m) { return GATE_UP || m * 4 * BM + 2 * BM < a.N; };
 
-    if (warp == 0) {
-        // ---------------- producer: this CTA's weight rows and half of the tokens
-        const uint64_t pol_w = tc::policy_evict_first();
-        const uint64_t pol_x = tc::policy_evict_last();
-        uint32_t it = 0;  // blocks loaded
-        bool ok = true;
-        for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
-            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-            const bool second = two(ti.m);
-            const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
-            const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
-            const int half = tokens_of(ti) / 2;
-            const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + half * BK);
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const uint32_t stage = it % STAGES;
-                if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u, abort_flag)) {
-                    give_up(c, a.status);
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
-                uint8_t* s = smem + stage * S::STAGE_BYTES;
-                if (tc::elect_one()) {
-                    if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
-                    tc::tma_load_2d_pair(s, &tmA, bar, kb * BK, w0, pol_w);
-                    if (second) tc::tma_load_2d_pair(s + A_BYTES, &tmA, bar, kb * BK, w1, pol_w);
-                    if (NM == 32)
-                        tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
-                                             ti.row0 + rank * CH, pol_x);
-                    else
-                        load_tokens(s + 2 * A_BYTES, tmB, bar, kb * BK, ti.row0 + rank * half,
-                                    half, pol_x);
-                }
-                __syncwarp();
-            }
-        }
-        // drain: this CTA's copies have landed (the even CTA's full barrier saw
-        // every byte of both CTAs when its last phase completed)
-        const int zero = 0;
-        for (uint32_t i = it < STAGES ? 0 : it - STAGES; i < it; ++i) {
-            const uint32_t stage = i % STAGES;
-            if (!tc::mbar_wait(leader ? &c.full[stage] : &c.empty[stage], (i / STAGES) & 1u, &zero))
-                atomicExch(a.status, MOE_ERR_TIMEOUT);
-        }
-    } else if (warp == 1) {
-        if (leader) {
-            // ---------------- MMA issuer (even CTA): 256 weight rows x n tokens, twice
-            uint32_t blk = 0;
-            bool ok = true;
-            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
-                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-                const bool second = two(ti.m);
-                const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, tokens_of(ti));
-                for (int kb = 0; kb < KB; ++kb, ++blk) {
-                    const uint32_t as = blk % ACC, stage = blk % STAGES;
-                    if (!tc::mbar_wait_warp(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
-                        !tc::mbar_wait_warp(&c.full[stage], (blk / STAGES) & 1u, abort_flag)) {
-                        give_up(c, a.status);
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after_sync();
-                    const uint32_t d = tmem_base + as * COLS;
-                    const uint32_t w = tc::smem_u32(smem + stage * S::STAGE_BYTES);
-                    if (tc::elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < BK / 32; ++k) {
-                            const uint64_t x = tc::desc_sw128(w + 2 * A_BYTES + k * 32);
-                            tc::mma_e4m3_pair(d, tc::desc_sw128(w + k * 32), x, idesc, k > 0);
-                            if (second)
-                                tc::mma_e4m3_pair(d + NM, tc::desc_sw128(w + A_BYTES + k * 32), x,
-                                                  idesc, k > 0);
-                        }
-                        tc::mma_commit_pair(&c.empty[stage], 0x3);
-                        tc::mma_commit_pair(&c.acc_full[as], 0x3);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (tc::elect_one()) tc::mma_commit_pair(&c.drain, 0x1);
-            __syncwarp();
-            const int zero = 0;
-            if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
-        }
-    } else if (warp == SCALE_WARP) {
-        // ---------------- factors: per block sx[token] * sw of this CTA's weight rows, U
-        // blocks loaded at a time. The ring runs ahead of the promotion, over tile
-        // borders too.
-        constexpr int U = 4, TPL = NM / 32;  // tokens per lane
-        const int nb_n = (a.N + 127) / 128;
-        const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
-        uint32_t blk = 0;
-        bool ok = true;
-        for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
-            const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-            const float* sxp = a.sx + (size_t)(ti.row0 + lane) * KB;
-            const float* swp[2];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int nb = min(first_row(ti.m, p) / BM, sw_rows - 1);
-                swp[p] = a.sw + ((size_t)ti.g * sw_rows + nb) * KB;
-            }
-            for (int k0 = 0; k0 < KB && ok; k0 += U) {
-                float x[TPL][U], w[2][U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool in = k0 + u < KB;
-                    w[0][u] = in ? swp[0][k0 + u] : 0.f;
-                    w[1][u] = in ? swp[1][k0 + u] : 0.f;
-#pragma unroll
-                    for (int i = 0; i < TPL; ++i)
-                        x[i][u] = in && lane + 32 * i < ti.len
-                                      ? sxp[(size_t)(32 * i) * KB + k0 + u] : 0.f;
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (k0 + u >= KB || !ok) continue;
-                    const uint32_t slot = blk % SLOTS;
-                    ok = tc::mbar_wait_warp(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u, abort_flag);
-                    if (!ok) {
-                        give_up(c, a.status);
-                        continue;
-                    }
-#pragma unroll
-                    for (int i = 0; i < TPL; ++i) {
-                        c.scales[slot][lane + 32 * i] = x[i][u] * w[0][u];
-                        c.scales[slot][NM + lane + 32 * i] = x[i][u] * w[1][u];
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
-                    ++blk;
-                }
-            }
-        }
-    } else if (warp >= PROMO_WARP) {
+    if (warp >= PROMO_WARP) {
+        if constexpr (NM == 128) tc::regs_inc<REGS_MANY>();
         // ---------------- promotion and epilogue: lane = one weight row of each
         // accumulator; group grp takes the tokens [grp * half, (grp + 1) * half), half of
         // the MMA's N, in chunks of 16
@@ -323,21 +198,32 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                     const uint32_t tb = lane_base + as * COLS + col0;
                     const float* sc = c.scales[slot] + col0;
 #pragma unroll
-                    for (int i = 0; i < NCH; ++i) {
+                    for (int i = 0; i < NCH; i += R) {
                         if (i * CH >= left) continue;
-                        uint32_t d0[CH], d1[CH];
-                        tc::tmem_ld16(tb + i * CH, d0);
-                        if (second) tc::tmem_ld16(tb + NM + i * CH, d1);
+                        uint32_t d0[R][CH], d1[R][CH];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            if (r > 0 && (i + r) * CH >= left) continue;
+                            tc::tmem_ld16(tb + (i + r) * CH, d0[r]);
+                            if (second) tc::tmem_ld16(tb + NM + (i + r) * CH, d1[r]);
+                        }
                         tc::tmem_ld_wait();
-                        tc::tmem_loaded(d0);
-                        if (second) tc::tmem_loaded(d1);
-                        if ((i + 1) * CH >= left) {  // the last chunk: the block is read
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            tc::tmem_loaded(d0[r]);
+                            tc::tmem_loaded(d1[r]);
+                        }
+                        if ((i + R) * CH >= left) {  // the last chunks: the block is read
                             tc::fence_before_sync();
                             __syncwarp();
                             if (lane == 0) tc::mbar_arrive_cluster_read(acc_empty0 + as * 8);
                         }
-                        promote(acc[0][i], d0, sc + i * CH);
-                        if (second) promote(acc[1][i], d1, sc + NM + i * CH);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            if (r > 0 && (i + r) * CH >= left) continue;
+                            promote(acc[0][i + r], d0[r], sc + (i + r) * CH);
+                            if (second) promote(acc[1][i + r], d1[r], sc + NM + (i + r) * CH);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&c.sc_empty[slot]);
@@ -448,6 +334,143 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 }
             }
         }
+    } else {
+        if constexpr (NM == 128) tc::regs_dec<REGS_FEW>();
+        if (warp == 0) {
+            // ---------------- producer: this CTA's weight rows and half of the tokens
+            const uint64_t pol_w = tc::policy_evict_first();
+            const uint64_t pol_x = tc::policy_evict_last();
+            uint32_t it = 0;  // blocks loaded
+            bool ok = true;
+            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
+                const bool second = two(ti.m);
+                const int w0 = ti.g * a.w_rows + first_row(ti.m, 0);
+                const int w1 = ti.g * a.w_rows + first_row(ti.m, 1);
+                const int half = tokens_of(ti) / 2;
+                const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + half * BK);
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const uint32_t stage = it % STAGES;
+                    if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u, abort_flag)) {
+                        give_up(c, a.status);
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = tc::map_to_cta(tc::smem_u32(&c.full[stage]), 0);
+                    uint8_t* s = smem + stage * S::STAGE_BYTES;
+                    if (tc::elect_one()) {
+                        if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
+                        tc::tma_load_2d_pair(s, &tmA, bar, kb * BK, w0, pol_w);
+                        if (second) tc::tma_load_2d_pair(s + A_BYTES, &tmA, bar, kb * BK, w1, pol_w);
+                        if (NM == 32)
+                            tc::tma_load_2d_pair(s + 2 * A_BYTES, &tmB.m[0], bar, kb * BK,
+                                                 ti.row0 + rank * CH, pol_x);
+                        else
+                            load_tokens(s + 2 * A_BYTES, tmB, bar, kb * BK, ti.row0 + rank * half,
+                                        half, pol_x);
+                    }
+                    __syncwarp();
+                }
+            }
+            // drain: this CTA's copies have landed (the even CTA's full barrier saw
+            // every byte of both CTAs when its last phase completed)
+            const int zero = 0;
+            for (uint32_t i = it < STAGES ? 0 : it - STAGES; i < it; ++i) {
+                const uint32_t stage = i % STAGES;
+                if (!tc::mbar_wait(leader ? &c.full[stage] : &c.empty[stage], (i / STAGES) & 1u, &zero))
+                    atomicExch(a.status, MOE_ERR_TIMEOUT);
+            }
+        } else if (warp == 1) {
+            if (leader) {
+                // ---------------- MMA issuer (even CTA): 256 weight rows x n tokens, twice
+                uint32_t blk = 0;
+                bool ok = true;
+                for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                    const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
+                    const bool second = two(ti.m);
+                    const uint32_t idesc = tc::idesc_e4m3_f32(2 * BM, tokens_of(ti));
+                    for (int kb = 0; kb < KB; ++kb, ++blk) {
+                        const uint32_t as = blk % ACC, stage = blk % STAGES;
+                        if (!tc::mbar_wait_warp(&c.acc_empty[as], ((blk / ACC) & 1u) ^ 1u, abort_flag) ||
+                            !tc::mbar_wait_warp(&c.full[stage], (blk / STAGES) & 1u, abort_flag)) {
+                            give_up(c, a.status);
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t d = tmem_base + as * COLS;
+                        const uint32_t w = tc::smem_u32(smem + stage * S::STAGE_BYTES);
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < BK / 32; ++k) {
+                                const uint64_t x = tc::desc_sw128(w + 2 * A_BYTES + k * 32);
+                                tc::mma_e4m3_pair(d, tc::desc_sw128(w + k * 32), x, idesc, k > 0);
+                                if (second)
+                                    tc::mma_e4m3_pair(d + NM, tc::desc_sw128(w + A_BYTES + k * 32), x,
+                                                      idesc, k > 0);
+                            }
+                            tc::mma_commit_pair(&c.empty[stage], 0x3);
+                            tc::mma_commit_pair(&c.acc_full[as], 0x3);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (tc::elect_one()) tc::mma_commit_pair(&c.drain, 0x1);
+                __syncwarp();
+                const int zero = 0;
+                if (!tc::mbar_wait(&c.drain, 0, &zero)) atomicExch(a.status, MOE_ERR_TIMEOUT);
+            }
+        } else if (warp == SCALE_WARP) {
+            // ---------------- factors: per block sx[token] * sw of this CTA's weight rows, U
+            // blocks loaded at a time. The ring runs ahead of the promotion, over tile
+            // borders too.
+            constexpr int U = NM == 128 ? 2 : 4, TPL = NM / 32;  // tokens per lane
+            const int nb_n = (a.N + 127) / 128;
+            const int sw_rows = GATE_UP ? 2 * nb_n : nb_n;
+            uint32_t blk = 0;
+            bool ok = true;
+            for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
+                const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
+                const float* sxp = a.sx + (size_t)(ti.row0 + lane) * KB;
+                const float* swp[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const int nb = min(first_row(ti.m, p) / BM, sw_rows - 1);
+                    swp[p] = a.sw + ((size_t)ti.g * sw_rows + nb) * KB;
+                }
+                for (int k0 = 0; k0 < KB && ok; k0 += U) {
+                    float x[TPL][U], w[2][U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool in = k0 + u < KB;
+                        w[0][u] = in ? swp[0][k0 + u] : 0.f;
+                        w[1][u] = in ? swp[1][k0 + u] : 0.f;
+#pragma unroll
+                        for (int i = 0; i < TPL; ++i)
+                            x[i][u] = in && lane + 32 * i < ti.len
+                                          ? sxp[(size_t)(32 * i) * KB + k0 + u] : 0.f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (k0 + u >= KB || !ok) continue;
+                        const uint32_t slot = blk % SLOTS;
+                        ok = tc::mbar_wait_warp(&c.sc_empty[slot], ((blk / SLOTS) & 1u) ^ 1u, abort_flag);
+                        if (!ok) {
+                            give_up(c, a.status);
+                            continue;
+                        }
+#pragma unroll
+                        for (int i = 0; i < TPL; ++i) {
+                            c.scales[slot][lane + 32 * i] = x[i][u] * w[0][u];
+                            c.scales[slot][NM + lane + 32 * i] = x[i][u] * w[1][u];
+                        }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&c.sc_full[slot]);
+                        ++blk;
+                    }
+                }
+            }
+        }
     }
 
     // Neither CTA leaves while the other may still signal its barriers or read
@@ -480,7 +503,7 @@ cudaError_t launch_nm(const BlockGemm& p, bool gate_up, cudaStream_t s) {
     CUtensorMap ma;
     TokenMaps mb;
     if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||
-        !make_token_byte_maps(&mb, p.xq, p.M, p.K, NM == 32 ? 1 : 2))
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K, boxes(NM)))
         return cudaErrorInvalidValue;
     if (gate_up) return launch<true, false, NM>(ma, mb, a, s);
     if (p.out_type == MOE_OUT_F32) return launch<false, true, NM>(ma, mb, a, s);
@@ -490,8 +513,9 @@ cudaError_t launch_nm(const BlockGemm& p, bool gate_up, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
-    return (long)p.M <= kFewRows32 * p.G ? launch_nm<32>(p, gate_up, s)
-                                         : launch_nm<64>(p, gate_up, s);
+    if ((long)p.M <= kFewRows32 * p.G) return launch_nm<32>(p, gate_up, s);
+    if ((long)p.M <= kFewRows64 * p.G) return launch_nm<64>(p, gate_up, s);
+    return launch_nm<128>(p, gate_up, s);
 }
 
 }  // namespace block
