@@ -456,7 +456,7 @@ cudaError_t launch_many(const BlockGemm& p, bool gate_up, cudaStream_t s) {
     const int w_rows = gate_up ? 2 * p.N : p.N;
     const int per_tile = gate_up ? BM : COLS;
     const Args a = {p.sx, p.sw, p.offsets, p.G, p.M, p.N, p.K, (p.N + per_tile - 1) / per_tile,
-                    w_rows, p.out, p.out_scales, p.status};
+                    w_rows, p.out, p.out_scales, p.status, nullptr, 0};
     CUtensorMap ma;
     TokenMaps mb;
     if (!make_byte_map(&ma, p.wq, (uint64_t)p.G * w_rows, p.K, BM) ||

@@ -46,8 +46,9 @@ template <bool PERMUTE>
 __global__ void __launch_bounds__(WARPS * 32, CTAS_PER_SM)
 block_quant_kernel(const __nv_bfloat16* __restrict__ x, long ldx, int M, int K,
                    const int* __restrict__ row_of, int kk, long R, uint8_t* __restrict__ codes,
-                   float* __restrict__ scales) {
+                   float* __restrict__ scales, int* clear) {
     pdl_launch_and_wait();
+    if (PERMUTE && clear && blockIdx.x == 0 && threadIdx.x == 0) *clear = 0;
     constexpr int U = 4;
     const int lane = threadIdx.x & 31;
     const int kb = (K + 127) / 128, chunks = (K + CHUNK - 1) / CHUNK;
@@ -105,16 +106,16 @@ cudaError_t launch_block_quant(const void* x, long ldx, int M, int K, void* code
     const cudaError_t err = launch_pdl(
         block_quant_kernel<false>, dim3(grid_of(M, K)), dim3(WARPS * 32), 0, s,
         static_cast<const __nv_bfloat16*>(x), ldx, M, K, (const int*)nullptr, 1, 0L,
-        static_cast<uint8_t*>(codes), scales);
+        static_cast<uint8_t*>(codes), scales, (int*)nullptr);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 cudaError_t launch_block_permute(const void* x, const int32_t* row_of, int T, int kk, int d,
-                                 long R, void* codes, float* scales, cudaStream_t s) {
+                                 long R, void* codes, float* scales, int* clear, cudaStream_t s) {
     const cudaError_t err = launch_pdl(
         block_quant_kernel<true>, dim3(grid_of(T, d)), dim3(WARPS * 32), 0, s,
         static_cast<const __nv_bfloat16*>(x), (long)d, T, d, row_of, kk, R,
-        static_cast<uint8_t*>(codes), scales);
+        static_cast<uint8_t*>(codes), scales, clear);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -309,7 +309,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
 template <int NT, bool OUT_F32>
 cudaError_t launch(const BlockGemm& p, int S, cudaStream_t s) {
-    const Args a = {p.sx, p.sw, nullptr, 1, p.M, p.N, p.K, 0, p.N, p.out, nullptr, p.status};
+    const Args a = {p.sx, p.sw, nullptr, 1, p.M, p.N, p.K, 0, p.N, p.out, nullptr, p.status,
+                    nullptr, 0};
     CUtensorMap ma;
     TokenMaps mb;
     if (!make_byte_map(&ma, p.wq, p.N, p.K, BM) || !make_token_byte_maps(&mb, p.xq, p.M, p.K, p.M <= 16 ? 1 : NT == 32 ? 2 : 4))

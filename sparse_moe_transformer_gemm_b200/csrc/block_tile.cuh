@@ -27,6 +27,8 @@ struct Args {
     void* out;
     float* out_scales;
     int* status;
+    const uint8_t* pf;   // weights to pull into L2 before the wait for the previous kernel
+    long long pf_bytes;
 };
 
 // Token rows [M, K] bytes, boxes of 16, 32, 64 and 128 rows x 128 bytes.

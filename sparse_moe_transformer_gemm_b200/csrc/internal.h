@@ -203,8 +203,9 @@ cudaError_t launch_select(const moe_config& c, const float* logits, long ld,
 // FP8 with a scale per block of 128: block_quant.cu, block_gemm.cu.
 cudaError_t launch_block_quant(const void* x, long ldx, int M, int K, void* codes, float* scales,
                                cudaStream_t s);
+// clear: a status word to set to 0 on the way (nullable).
 cudaError_t launch_block_permute(const void* x, const int32_t* row_of, int T, int kk, int d,
-                                 long R, void* codes, float* scales, cudaStream_t s);
+                                 long R, void* codes, float* scales, int* clear, cudaStream_t s);
 // A grouped product; rows past offsets[G] are not written. offsets NULL: one
 // group of all M rows. gate_up: N = d_ff output features, the weights hold
 // 2 * N rows (gate, up) and the output is hq [M, N] codes with sh [M, N/128].

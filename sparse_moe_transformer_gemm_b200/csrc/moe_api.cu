@@ -286,10 +286,12 @@ bool gather_batch(const moe_config* c) {
     return (long long)c->T * (c->k + shared_slots(*c)) <= MOE_GATHER_MAX_SLOTS;
 }
 
-// The layer after its router, from the routing idx / w.
+// The layer after its router, from the routing idx / w. clear_status: nothing has
+// reset the status word yet (the block-FP8 path does it in a kernel of its own: a
+// memset is a launch).
 int forward_routed(const moe_config* cfg, const void* x, const int32_t* idx, const float* w,
                    const void* w_gate_up, const void* s_gate_up, const void* w_down,
-                   const void* s_down, void* out, void* ws, cudaStream_t s) {
+                   const void* s_down, void* out, void* ws, bool clear_status, cudaStream_t s) {
     const WsLayout L = ws_layout(*cfg);
     int32_t* offsets = at<int32_t>(ws, L.offsets);
     int32_t* row_of = at<int32_t>(ws, L.row_of);
@@ -305,10 +307,13 @@ int forward_routed(const moe_config* cfg, const void* x, const int32_t* idx, con
         MOE_TRY(cuda_status(
             launch_permute_index(*cfg, idx, counts, offsets, row_of, tok, hist, rank, s)));
         MOE_TRY(cuda_status(launch_block_permute(x, row_of, g.T, g.k, g.d, (long)g.T * g.k, xperm,
-                                                 scales_after(xperm, g, g.d), s)));
+                                                 scales_after(xperm, g, g.d),
+                                                 clear_status ? at<int>(ws, L.status) : nullptr,
+                                                 s)));
         MOE_TRY(block_experts(cfg, offsets, w_gate_up, s_gate_up, w_down, s_down, y, ws, s));
         return cuda_status(launch_combine(*cfg, y, row_of, w, out, s));
     }
+    if (clear_status) MOE_TRY(cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), s)));
     if (gather_batch(cfg)) {
         MOE_TRY(cuda_status(
             launch_permute_index(*cfg, idx, counts, offsets, row_of, tok, hist, rank, s)));
@@ -488,7 +493,8 @@ int moe_forward3(const moe_config* cfg, const void* x, const void* w_gate, const
     float* w = at<float>(ws, L.w);
     MOE_TRY(cuda_status(cudaMemsetAsync(ws, 0, L.control_end, s)));
     MOE_TRY(cuda_status(route(cfg, x, w_gate, gate_bias, opt, idx, w, ws, s)));
-    return forward_routed(cfg, x, idx, w, w_gate_up, s_gate_up, w_down, s_down, out, ws, s);
+    return forward_routed(cfg, x, idx, w, w_gate_up, s_gate_up, w_down, s_down, out, ws, false,
+                          s);
 }
 
 int moe_forward4(const moe_config* cfg, const void* x, const void* w_gate, const float* gate_bias,
@@ -509,7 +515,8 @@ int moe_forward4(const moe_config* cfg, const void* x, const void* w_gate, const
     MOE_TRY(cuda_status(cudaMemsetAsync(ws, 0, L.control_end, s)));
     MOE_TRY(cuda_status(route_grouped(cfg, x, w_gate, gate_bias, opt ? *opt : kNoOptions,
                                       grp ? *grp : kNoGroups, idx, w, ws, s)));
-    return forward_routed(cfg, x, idx, w, w_gate_up, s_gate_up, w_down, s_down, out, ws, s);
+    return forward_routed(cfg, x, idx, w, w_gate_up, s_gate_up, w_down, s_down, out, ws, false,
+                          s);
 }
 
 int moe_forward_routed(const moe_config* cfg, const void* x, const int32_t* topk_idx,
@@ -523,9 +530,8 @@ int moe_forward_routed(const moe_config* cfg, const void* x, const int32_t* topk
     MOE_TRY(check_expert_weights(cfg, w_down, s_down));
     MOE_TRY(check_ws(cfg, ws, ws_bytes));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    MOE_TRY(cuda_status(cudaMemsetAsync(ws, 0, sizeof(int32_t), s)));
     return forward_routed(cfg, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, out, ws,
-                          s);
+                          true, s);
 }
 
 int moe_select(const moe_config* cfg, const float* logits, int64_t ld,
@@ -592,7 +598,7 @@ int moe_block_permute(const moe_config* cfg, const void* x, const int32_t* row_o
     if (!x || !row_of || !xq || !sx || !aligned16(x) || !aligned16(xq)) return MOE_ERR_INVALID_ARG;
     const moe_config g = grouped_config(*cfg);
     return cuda_status(launch_block_permute(x, row_of, g.T, g.k, g.d, (long)g.T * g.k, xq, sx,
-                                            static_cast<cudaStream_t>(stream)));
+                                            nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_block_gate_up(const moe_config* cfg, const void* xq, const float* sx,
