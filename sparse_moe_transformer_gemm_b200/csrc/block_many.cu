@@ -33,6 +33,8 @@
 // lanes; groups 0 and 1 the first half, 2 and 3 the second). The promotion's
 // threads hold 96 values, so the first four warps hand registers over
 // (setmaxnreg). All waits are bounded.
+#include <type_traits>
+
 #include "block_tile.cuh"
 
 namespace moe {
@@ -51,8 +53,7 @@ constexpr int CH = 32;                 // columns per tcgen05.ld
 constexpr int SCALE_WARP = 2;
 constexpr int FB = 4;                  // blocks per slot of the factor ring
 constexpr int SLOTS = 2;
-constexpr int EPI_COLS = 16;           // columns per pass of the store staging
-constexpr int EPI_BYTES = 4 * GROUPS * 32 * EPI_COLS * 2;  // [32 tokens][16 columns] bf16 per warp
+constexpr int EPI_BYTES = 4 * GROUPS * 32 * 32;  // a [32 tokens][32 bytes] store tile per warp
 // registers a thread: 96 at launch; 5 * 96 = 32 + 4 * 112
 constexpr int REGS_FEW = 32, REGS_MANY = 112;
 static_assert(REGS_FEW + GROUPS * REGS_MANY == (1 + GROUPS) * 96, "no more than the launch gave");
@@ -251,50 +252,53 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 const int n0 = ti.m * COLS + side * 128 + half * 2 * CH;  // first output column
                 const int rows = ti.len - rank * BM - quad * 32; // tokens of this warp
                 const long r0 = ti.row0 + rank * BM + quad * 32;
-                if (!OUT_F32 && a.N % 8 == 0) {
-                    // 16 columns at a time through the warp's [32 tokens][16 columns]
-                    // tile, its 16-byte halves swapped for every other four tokens (no
-                    // bank conflicts): whole 32-byte sectors go out, two lanes a row
-                    uint4* st = reinterpret_cast<uint4*>(
-                        epi + (warp - PROMO_WARP) * (EPI_BYTES / (4 * GROUPS)));
+                // EC columns at a time through the warp's [32 tokens][32 bytes] tile, its
+                // 16-byte halves swapped for every other four tokens (no bank conflicts):
+                // whole 32-byte sectors go out, two lanes a row
+                using Out = typename std::conditional<OUT_F32, float, uint16_t>::type;
+                constexpr int EC = 32 / sizeof(Out), PIECE = 16 / sizeof(Out);
+                const bool vec = a.N % PIECE == 0;
+                uint4* st = reinterpret_cast<uint4*>(
+                    epi + (warp - PROMO_WARP) * (EPI_BYTES / (4 * GROUPS)));
 #pragma unroll
-                    for (int i = 0; i < 2 * CH / EPI_COLS; ++i) {
-                        __syncwarp();  // the previous pass is read
+                for (int i = 0; i < 2 * CH / EC; ++i) {
+                    __syncwarp();  // the previous pass is read
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const auto& v = acc[i / (CH / EPI_COLS)];
-                            const int j = (i % (CH / EPI_COLS)) * EPI_COLS + q * 8;
-                            st[lane * 2 + (q ^ ((lane >> 2) & 1))] = make_uint4(
-                                pack_bf16x2(value_at(v, j), value_at(v, j + 1)),
-                                pack_bf16x2(value_at(v, j + 2), value_at(v, j + 3)),
-                                pack_bf16x2(value_at(v, j + 4), value_at(v, j + 5)),
-                                pack_bf16x2(value_at(v, j + 6), value_at(v, j + 7)));
-                        }
-                        __syncwarp();
+                    for (int q = 0; q < 2; ++q) {
+                        const auto& v = acc[i / (CH / EC)];
+                        const int j = (i % (CH / EC)) * EC + q * PIECE;
+                        uint4 u;
+                        if constexpr (OUT_F32)
+                            u = make_uint4(f32_bits(value_at(v, j)), f32_bits(value_at(v, j + 1)),
+                                           f32_bits(value_at(v, j + 2)),
+                                           f32_bits(value_at(v, j + 3)));
+                        else
+                            u = make_uint4(pack_bf16x2(value_at(v, j), value_at(v, j + 1)),
+                                           pack_bf16x2(value_at(v, j + 2), value_at(v, j + 3)),
+                                           pack_bf16x2(value_at(v, j + 4), value_at(v, j + 5)),
+                                           pack_bf16x2(value_at(v, j + 6), value_at(v, j + 7)));
+                        st[lane * 2 + (q ^ ((lane >> 2) & 1))] = u;
+                    }
+                    __syncwarp();
+                    Out* o = static_cast<Out*>(a.out) + r0 * a.N + n0 + i * EC;
+                    if (vec) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const int n = q * 16 + (lane >> 1), ch = lane & 1;
-                            const int col = n0 + i * EPI_COLS + ch * 8;
-                            if (n < rows && col < a.N)
-                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                                          (r0 + n) * a.N + col) =
+                            if (n < rows && n0 + i * EC + ch * PIECE < a.N)
+                                *reinterpret_cast<uint4*>(o + (long)n * a.N + ch * PIECE) =
                                     st[n * 2 + (ch ^ ((n >> 2) & 1))];
                         }
+                    } else {
+                        // rows that are not 16-byte aligned: by elements, still in order
+#pragma unroll 1
+                        for (int e = lane; e < 32 * EC; e += 32) {
+                            const int n = e / EC, c0 = e % EC, ch = c0 / PIECE;
+                            if (n < rows && n0 + i * EC + c0 < a.N)
+                                o[(long)n * a.N + c0] = reinterpret_cast<const Out*>(
+                                    st + n * 2 + (ch ^ ((n >> 2) & 1)))[c0 % PIECE];
+                        }
                     }
-                } else if (mine) {
-                    const size_t at = (size_t)(ti.row0 + tok) * a.N + n0;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int j = 0; j < CH; ++j)
-                            if (n0 + i * CH + j < a.N) {
-                                if (OUT_F32)
-                                    static_cast<float*>(a.out)[at + i * CH + j] =
-                                        value_at(acc[i], j);
-                                else
-                                    static_cast<uint16_t*>(a.out)[at + i * CH + j] =
-                                        float_to_bf16_bits(value_at(acc[i], j));
-                            }
                 }
             }
         }

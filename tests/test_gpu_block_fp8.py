@@ -112,7 +112,11 @@ def product(q, s, wq, sw, N, dtype=torch.bfloat16, offsets=None, fill=-99.0):
 SIZES = [(1, 1, 16), (1, 128, 128), (1, 4096, 4096), (2, 130, 144), (7, 500, 2064),
          (16, 256, 256), (17, 520, 640), (31, 129, 1040), (33, 257, 384), (64, 1024, 4096),
          (65, 512, 512), (100, 1, 256), (128, 640, 1536), (129, 384, 128), (200, 1000, 912),
-         (300, 513, 272), (1000, 768, 2048)]
+         (300, 513, 272), (1000, 768, 2048),
+         # enough tiles for the pair kernels: tokens in the MMA's rows, ...
+         (1300, 1301, 144), (1300, 1400, 272), (1537, 1284, 528),
+         # ... or weights, in tiles of up to 32, 64 and 128 tokens
+         (20, 19000, 128), (40, 19001, 144), (100, 19004, 272), (128, 19200, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -126,9 +130,11 @@ def test_product(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("counts", [[3, 0, 5, 1], [0, 0, 0, 0], [200, 1, 0, 33],
-                                    [0, 129, 128, 127], [16, 17, 31, 32, 64, 65, 0, 1]])
-@pytest.mark.parametrize("N,K", [(256, 384), (200, 144), (640, 1024)])
-def test_grouped_product_leaves_other_rows(counts, N, K):
+                                    [0, 129, 128, 127], [16, 17, 31, 32, 64, 65, 0, 1],
+                                    [300, 0, 129, 513], [257, 256, 255, 1], [40, 64, 33, 65]])
+@pytest.mark.parametrize("N,K", [(256, 384), (200, 144), (640, 1024), (333, 272)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_grouped_product_leaves_other_rows(counts, N, K, dtype):
     g = gen(sum(counts) + N)
     G, pad = len(counts), 5
     offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32) + 2
@@ -136,7 +142,7 @@ def test_grouped_product_leaves_other_rows(counts, N, K):
     q, s = quantised(activations(g, M, K))
     ws = [ref.random_weight(g, N, K) for _ in range(G)]
     wq, sw = torch.stack([w for w, _ in ws]), torch.stack([v for _, v in ws])
-    out = product(q, s, wq, sw, N, offsets=offsets)
+    out = product(q, s, wq, sw, N, dtype, offsets)
     xv = ref.values(q, s)
     at = 2
     for e, n in enumerate(counts):
@@ -144,6 +150,33 @@ def test_grouped_product_leaves_other_rows(counts, N, K):
             ref.check_product(out[at:at + n], xv[at:at + n], ref.weight_values(wq[e], sw[e]), e)
         at += n
     assert (out[:2] == -99).all() and (out[at:] == -99).all()
+
+
+def test_outputs_past_two_to_the_31_elements_and_more_tiles_than_a_list_holds():
+    """131075 x 20008 (2.6e9 outputs, 40527 tiles), rows from all over checked."""
+    g = gen(30)
+    M, N, K = 131075, 20008, 16
+    q, s = quantised(activations(g, M, K))
+    wq, sw = ref.random_weight(g, N, K)
+    out = product(q, s, wq, sw, N)
+    rows = torch.cat([torch.arange(0, 5), torch.randint(0, M, (200,)),
+                      torch.arange(M - 5, M)]).to("cuda")
+    ref.check_product(out[rows], ref.values(q[rows], s[rows]), ref.weight_values(wq, sw))
+
+
+def test_more_weight_tiles_than_a_list_holds():
+    """256 groups of one row times 131072 weight rows: 65536 tiles of the few-rows kernel."""
+    g = gen(31)
+    G, N, K = 256, 131072, 16
+    q, s = quantised(activations(g, G, K))
+    wq = torch.randint(0, 256, (G, N, K), generator=g, device="cuda", dtype=torch.uint8)
+    wq = torch.where(wq & 0x7F == 0x7F, 0, wq).to(torch.uint8)
+    sw = torch.rand(G, N // 128, 1, generator=g, device="cuda") + 0.5
+    offsets = torch.arange(G + 1, dtype=torch.int32, device="cuda")
+    out = product(q, s, wq, sw, N, offsets=offsets)
+    xv = ref.values(q, s)
+    for e in (0, 1, 100, 254, 255):
+        ref.check_product(out[e:e + 1], xv[e:e + 1], ref.weight_values(wq[e], sw[e]), e)
 
 
 def test_grouped_product_clamps_offsets():
@@ -292,7 +325,8 @@ def check_h(hq, sh, xv, wv, F):
 
 LAYERS = [(1, 128, 1, 1, 128), (1, 512, 8, 4, 256), (5, 256, 4, 4, 384), (64, 512, 16, 4, 128),
           (77, 384, 6, 2, 640), (300, 256, 3, 2, 256), (513, 640, 2, 1, 384),
-          (40, 1024, 64, 8, 256)]
+          (40, 1024, 64, 8, 256), (100, 256, 8, 3, 384), (200, 384, 4, 2, 256),
+          (1100, 256, 8, 2, 640), (3, 8192, 4, 2, 128), (260, 128, 255, 1, 128)]
 
 
 @pytest.mark.parametrize("T,d,E,k,F", LAYERS)
