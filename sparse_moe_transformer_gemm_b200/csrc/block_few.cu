@@ -3,23 +3,27 @@
 //
 // The weight stream is the bound: every weight byte is read once and used for a
 // handful of tokens. The weight rows are the MMA's M (256 a pair and
-// accumulator, 128 a CTA) and up to 32 tokens its N, so a tile costs the tensor
-// core little; two accumulators share the staged tokens (gate_up: gate and up
-// rows, whose SiLU(g) u is then formed in registers; a plain product: two
-// 256-row tiles). A block's sums take 64 TMEM columns, so eight blocks are in
-// flight between the MMAs and the promotion, and the ring holds 6 x 32 KB of
-// weights per SM. (With two blocks in flight, which larger token tiles leave
-// room for, each block waited for the promotion's round trip: the Hy3 experts
-// at T = 64 took 740 us.)
+// accumulator, 128 a CTA) and up to NM = 32, 64 or 128 tokens its N, so a tile
+// costs the tensor core little; two accumulators share the staged tokens
+// (gate_up: gate and up rows, whose SiLU(g) u is then formed in registers; a
+// plain product: two 256-row tiles). A block's sums take 2 NM TMEM columns, so 8,
+// 4 or 2 blocks are in flight between the MMAs and the promotion, and the ring
+// holds 6, 5 or 4 stages of 32 KB of weights per SM.
 //
-// A thread of the promotion owns one weight row and 16 tokens of each
+// NM is the smallest that holds most groups' rows, so that each weight byte is read
+// once; a smaller one keeps more blocks in flight. The experts d = 4096, d_ff =
+// 1536, E = 192, top-8, whole layer: T = 64 (2.7 rows a group) 514 us with NM =
+// 32, 740 with 128; T = 1024 (43 rows) 654 with 64, 705 with 32; T = 1536 (64 rows)
+// 664 with 128, 805 with 32. At T = 64 the layer reads 3.4 GB: 6.6 TB/s.
+//
+// A thread of the promotion owns one weight row and NM / 2 tokens of each
 // accumulator. A CTA's 128 weight rows of an accumulator lie in one block of
 // rows, so the factor sx[token] sw[rows] of a token is the same for the whole
 // CTA: a warp forms them in a ring in shared memory, ahead of the promotion.
 //
 // Per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM owner (+ MMA issuer in
 // the even CTA), warp 2 the factors, warps 4-11 promotion and epilogue in two
-// groups of four (one warp per TMEM lane quarter) with 16 tokens each. All
+// groups of four (one warp per TMEM lane quarter) with NM / 2 tokens each. All
 // waits are bounded.
 #include "block_tile.cuh"
 
@@ -31,20 +35,29 @@ constexpr int BM = 128;                // weight rows per CTA and accumulator
 constexpr int A_BYTES = BM * BK;
 constexpr int CH = 16;                 // tokens per promotion chunk
 constexpr int SLOTS = 8;               // factor ring
+// Blocks a CTA loads ahead of the MMAs where a pair has several tiles: enough to cover
+// the latency; with more of them in flight HBM serves all of them more slowly. The
+// layer of the header with 4 and with the whole ring (6 or 5): T = 64 503 and 519 us,
+// T = 256 546 and 559, T = 512 577 and 597, T = 1024 612 and 650; 3: 508, 560, 594, 640.
+// One token, whose 8 experts give a pair one tile or none, takes 51.0 with 4, 49.9 with 6.
+constexpr uint32_t AHEAD = 4;
 constexpr int SCALE_WARP = 2, PROMO_WARP = 4;
 constexpr int THREADS = 32 * (PROMO_WARP + 8);
 // Registers a thread with tiles of 128 tokens, whose promotion holds 128
 // accumulators: 168 at launch; 3 * 168 = 72 + 2 * 216.
 constexpr int REGS_FEW = 72, REGS_MANY = 216;
 static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
-// up to so many rows a group on average, tiles of 32 and of 64 tokens
+// Up to so many rows a group on average, tiles of 32 and of 64 tokens: the layer of
+// the header at T = 512 (21 rows) takes 590 us with 64 and 620 with 32, at 1536
+// (64 rows) 664 with 128 and 700 with 64.
 constexpr long kFewRows32 = 20, kFewRows64 = 56;
 
 // NM: tokens per pair tile at most.
 template <int NM>
 struct Shape {
     static constexpr int STAGE_BYTES = 2 * A_BYTES + NM / 2 * BK;  // 34 / 36 / 40 KB
-    static constexpr int STAGES = NM == 32 ? 6 : NM == 64 ? 5 : 4;
+    static constexpr int STAGES = NM == 32 ? 6 : NM == 64 ? 5 : 4;  // what fits
+    static_assert(STAGES >= (int)AHEAD);
     static constexpr int COLS = 2 * NM;     // TMEM columns per block
     static constexpr int ACC = 512 / COLS;  // blocks in flight
     static constexpr int NCH = NM / 2 / CH; // chunks of a group and accumulator
@@ -351,6 +364,7 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
             // ---------------- producer: this CTA's weight rows and half of the tokens
             const uint64_t pol_w = tc::policy_evict_first();
             const uint64_t pol_x = tc::policy_evict_last();
+            const uint32_t ahead = total > n_pairs ? AHEAD : STAGES;
             uint32_t it = 0;  // blocks loaded
             bool ok = true;
             for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
@@ -362,7 +376,11 @@ block_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                 const uint32_t bytes = 2u * ((second ? 2 : 1) * A_BYTES + half * BK);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const uint32_t stage = it % STAGES;
-                    if (!tc::mbar_wait_warp(&c.empty[stage], ((it / STAGES) & 1u) ^ 1u, abort_flag)) {
+                    // (blocks are released in order: the one before the last that may be in
+                    // flight is read, so the one that had this stage is too)
+                    const uint32_t old = it - ahead;
+                    if (it >= ahead &&
+                        !tc::mbar_wait_warp(&c.empty[old % STAGES], (old / STAGES) & 1u, abort_flag)) {
                         give_up(c, a.status);
                         ok = false;
                         break;

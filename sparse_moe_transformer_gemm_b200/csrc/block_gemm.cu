@@ -7,7 +7,7 @@
 //
 // The kernels let the tensor core sum one block of 128 columns at a time into TMEM
 // and add it, scaled, to fp32 registers. They differ in what the MMA's rows are:
-// weight rows with up to 32 tokens as its columns, on pairs of SMs (block_few.cu);
+// weight rows with up to 128 tokens as its columns, on pairs of SMs (block_few.cu);
 // tokens with 256 weight rows as its columns, on pairs (block_many.cu); or weight
 // rows on single SMs that share the columns of K (block_split.cu), for one product
 // that is too small to give every pair a tile.
