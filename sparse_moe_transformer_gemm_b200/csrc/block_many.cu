@@ -46,7 +46,10 @@ namespace {
 constexpr int BM = 128;                // tokens, and weight rows, a CTA stages
 constexpr int NM = 2 * BM;             // tokens per pair tile
 constexpr int STAGE_BYTES = 2 * BM * BK;
-constexpr int STAGES = 6;
+// 6 would fit. Fewer blocks in flight are served faster by HBM: the experts d = 4096,
+// d_ff = 1536, E = 192, top-8 at T = 4096 take 1190 us with 5 and 1209 with 6, at T =
+// 8192 2354 and 2398; with 4 1182 and 2340, but 2048 x 8192 x 4096 takes 90 us for 85.
+constexpr int STAGES = 5;
 constexpr int COLS = 256;              // TMEM columns per block
 constexpr int GROUPS = 4;              // promotion groups of 4 warps
 constexpr int PROMO_WARP = 4;          // the first of 16
