@@ -25,8 +25,8 @@
 // warp-uniform control flow (the MMA warp alone had needed 1000 cycles a block), the
 // factors waited for once in 4 blocks and four promotion groups in place of two with
 // 128 columns a thread 346 us; halves with an issuing warp each 305 us; a tile
-// looked up once and waits as one short loop 282 us (1.95 PFLOP/s; 330 us on a box
-// at its power cap, 1.5 GHz). 128 weight rows a tile with four accumulators in
+// looked up once and waits as one short loop 282 us (1.95 PFLOP/s; 326 us after
+// a second of load, at the power cap). 128 weight rows a tile with four accumulators in
 // flight: 507 us. Tensor pipe 44% active.
 //
 // Per CTA (640 threads): warp 0 TMA producer, warps 1 and 3 (even CTA) MMA issuers of
@@ -317,12 +317,12 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             bool ok = true;
             for (int t = pair, i_t = 0; t < total && ok; t += n_pairs, ++i_t) {
                 const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-                // the rows that exist, in 16-row boxes (what the rest of the stage
-                // holds only reaches TMEM lanes that nobody reads)
-                const int r0 = (min(ti.len, BM) + 15) & ~15;
-                const int r1 = (max(ti.len - BM, 0) + 15) & ~15;
-                const int rows = leader ? r0 : r1;
-                const uint32_t bytes = (uint32_t)(2 * BM + r0 + r1) * BK;
+                // the rows that exist, in 16-row boxes; the others, which only reach TMEM
+                // lanes that nobody reads, as zeros from past the end of the array (left as
+                // they were they cost power: experts T = 8192 2770 us against 2735 after a
+                // second of load, 2370 and 2360 before)
+                const int rows = (min(max(ti.len - rank * BM, 0), BM) + 15) & ~15;
+                constexpr uint32_t bytes = 2 * STAGE_BYTES;
                 const int w0 = ti.g * a.w_rows +
                                (GATE_UP ? ti.m * BM + rank * a.N : ti.m * COLS + rank * BM);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
@@ -339,6 +339,7 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         if (leader) tc::mbar_arrive_expect_tx(&c.full[stage], bytes);
                         tc::tma_load_2d_pair(s + BM * BK, &tmA, bar, kb * BK, w0, pol_w);
                         load_tokens(s, tmB, bar, kb * BK, ti.row0 + rank * BM, rows, pol_x);
+                        load_tokens(s + rows * BK, tmB, bar, kb * BK, a.M, BM - rows, pol_x);
                     }
                     __syncwarp();
                 }
