@@ -7,11 +7,12 @@
 // a cluster take K / S of its columns each, so that N = 4096 has 32 S tiles. Each CTA
 // adds its blocks to fp32 registers as block_few.cu does, leaves the partial sums
 // in shared memory, and after a cluster barrier CTA r adds the S partial sums of the
-// tokens r, r + S, ... in a fixed order, through distributed shared memory.
+// tokens r, r + S, ... in a fixed order, through distributed shared memory, a warp per
+// token with 16 bytes a lane (by single floats 128 x 4096 x 4096 took 11.3 us).
 //
 // The bound is latency: the loads of the ring's first stages, the walk over K / S,
-// the exchange. Measured: 1 x 4096 x 4096 in 6.6 us (the pair kernel: 14), 128 x
-// 4096 x 4096 in 11.
+// the exchange. Measured: 1 x 4096 x 4096 in 6.5 us (the pair kernel: 13), 128 x
+// 4096 x 4096 in 10 (31).
 //
 // Per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA issuer,
 // warp 2 the factors sx[token] sw, warps 4-11 promotion in two groups of four (one
@@ -276,27 +277,49 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     }
     tc::cluster_sync();
     {
-        // thread: weight row `row`, of CTA split's tokens every third one (three thirds
-        // of the block); the S partial sums in the order of the slices
+        // a warp takes one token at a time, of CTA split's every S-th, a lane 4 weight rows of
+        // it; the S partial sums in the order of the slices
         const uint32_t base = tc::smem_u32(part);
         uint32_t from[8];
 #pragma unroll
         for (int sp = 0; sp < 8; ++sp) from[sp] = tc::map_to_cta(base, sp < S ? sp : 0);
-        for (int t = split + (threadIdx.x >> 7) * S; t < len; t += THREADS / 128 * S) {
-            const uint32_t off = (uint32_t)(t * BM + row) * 4u;
-            float v[8];
+        const int r4 = lane * 4, valid = a.N - (w0 + r4);  // valid rows of this lane
+        for (int t = split + warp * S; t < len; t += THREADS / 32 * S) {
+            const uint32_t off = (uint32_t)(t * BM + r4) * 4u;
+            float4 v[8];
 #pragma unroll
-            for (int sp = 0; sp < 8; ++sp) v[sp] = sp < S ? tc::ld_cluster_f32(from[sp] + off) : 0.f;
-            float sum = v[0];
+            for (int sp = 0; sp < 8; ++sp)
+                if (sp < S) v[sp] = tc::ld_cluster_f32x4(from[sp] + off);
+            float4 sum = v[0];
 #pragma unroll
             for (int sp = 1; sp < 8; ++sp)
-                if (sp < S) sum += v[sp];
-            if (w0 + row < a.N) {
-                const size_t at = (size_t)(row0 + t) * a.N + w0 + row;
-                if (OUT_F32)
-                    static_cast<float*>(a.out)[at] = sum;
+                if (sp < S) {
+                    sum.x += v[sp].x;
+                    sum.y += v[sp].y;
+                    sum.z += v[sp].z;
+                    sum.w += v[sp].w;
+                }
+            if (valid <= 0) continue;
+            const size_t at = (size_t)(row0 + t) * a.N + w0 + r4;
+            const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+            if constexpr (OUT_F32) {
+                float* o = static_cast<float*>(a.out) + at;
+                if (a.N % 4 == 0)
+                    *reinterpret_cast<float4*>(o) = sum;
                 else
-                    static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(sum);
+                    for (int j = 0; j < 4; ++j)
+                        if (j < valid) o[j] = f[j];
+            } else {
+                uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+                if (a.N % 4 == 0) {
+                    uint16_t h[4];
+                    for (int j = 0; j < 4; ++j) h[j] = float_to_bf16_bits(f[j]);
+                    *reinterpret_cast<uint2*>(o) =
+                        make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
+                } else {
+                    for (int j = 0; j < 4; ++j)
+                        if (j < valid) o[j] = float_to_bf16_bits(f[j]);
+                }
             }
         }
     }
@@ -339,16 +362,16 @@ cudaError_t launch(const BlockGemm& p, int S, cudaStream_t s) {
 
 }  // namespace
 
-// One product whose tiles of 128 rows (and up to 32 tokens, or 128) leave SMs idle:
-// as many slices of K, at most 8 (the portable cluster size), as still run at once.
-// Past one tile of tokens the pair kernels read the weights once for more of them,
-// so there K has to be cut at least in two. Measured: 512 x 4096 x 4096 (128 tiles,
-// uncut) in about 35 us against 25.
+// One product whose tiles of 128 rows (and up to 32 tokens, or 128) fit the SMs at
+// once: as many slices of K, at most 8 (the portable cluster size), as still run at
+// once; 0 for more tiles than SMs. Measured against the pair kernels: 128 x 4096 x 4096
+// (32 tiles) 10.2 us and 31, 512 x 2048 x 4096 (64) 13.7 and 23, 512 x 4096 x 4096 (128,
+// uncut) 21.3 and 23.8, 200 x 256 x 128 (4, one block) 6.8 and 6.8.
 int splits(const BlockGemm& p) {
     if (p.offsets) return 0;
     const long token_tiles = p.M <= 32 ? 1 : (p.M + 127) / 128;
     const long tiles = (p.N + BM - 1) / BM * token_tiles, sms = 2L * sm_pairs();
-    if (tiles > (token_tiles == 1 ? sms : sms / 2)) return 0;
+    if (tiles > sms) return 0;
     const int KB = (p.K + BK - 1) / BK;
     int S = 1;
     while (S < 8 && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
