@@ -10,11 +10,18 @@
 // 4 or 2 blocks are in flight between the MMAs and the promotion, and the ring
 // holds 6, 5 or 4 stages of 32 KB of weights per SM.
 //
-// NM is the smallest that holds most groups' rows, so that each weight byte is read
-// once; a smaller one keeps more blocks in flight. The experts d = 4096, d_ff =
-// 1536, E = 192, top-8, whole layer: T = 64 (2.7 rows a group) 514 us with NM =
-// 32, 740 with 128; T = 1024 (43 rows) 654 with 64, 705 with 32; T = 1536 (64 rows)
-// 664 with 128, 805 with 32. At T = 64 the layer reads 3.4 GB: 6.6 TB/s.
+// NM = 32 for up to a row a group on average, 64 for up to 32 rows, 128 beyond: a
+// group in one tile has its weights read once, a smaller tile keeps more blocks in
+// flight and is done sooner. The experts d = 4096, d_ff = 1536, E = 192, top-8,
+// whole layer, tokens evenly over the experts / expert e's share falling as e^-0.5:
+//              32           64            128
+//   T = 1      50           51            53
+//   T = 64     503 / 456    505 / 456     508 / 465
+//   T = 256    547 / 557    548 / 548     552 / 552
+//   T = 512    578 / 616    579 / 597     587 / 598
+//   T = 1024   725 / 742    616 / 681     625 / 668
+//   T = 2048   1038 / 1121  1020 / 918    743 / 855 us
+// At T = 64 the layer reads 3.4 GB: 6.7 TB/s.
 //
 // A thread of the promotion owns one weight row and NM / 2 tokens of each
 // accumulator. A CTA's 128 weight rows of an accumulator lie in one block of
@@ -47,10 +54,8 @@ constexpr int THREADS = 32 * (PROMO_WARP + 8);
 // accumulators: 168 at launch; 3 * 168 = 72 + 2 * 216.
 constexpr int REGS_FEW = 72, REGS_MANY = 216;
 static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
-// Up to so many rows a group on average, tiles of 32 and of 64 tokens: the layer of
-// the header at T = 512 (21 rows) takes 590 us with 64 and 620 with 32, at 1536
-// (64 rows) 664 with 128 and 700 with 64.
-constexpr long kFewRows32 = 20, kFewRows64 = 56;
+// Up to so many rows a group on average, tiles of 64 tokens.
+constexpr long kFewRows64 = 32;
 
 // NM: tokens per pair tile at most.
 template <int NM>
@@ -553,7 +558,7 @@ cudaError_t launch_nm(const BlockGemm& p, bool gate_up, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s) {
-    if ((long)p.M <= kFewRows32 * p.G) return launch_nm<32>(p, gate_up, s);
+    if (p.M <= p.G || (!p.offsets && p.M <= 32)) return launch_nm<32>(p, gate_up, s);
     if ((long)p.M <= kFewRows64 * p.G) return launch_nm<64>(p, gate_up, s);
     return launch_nm<128>(p, gate_up, s);
 }
