@@ -432,6 +432,9 @@ MOE_API int moe_block_quant(const void* x, int64_t ldx, int32_t M, int32_t K, vo
  * (values outside are clamped): rows [offsets[g], offsets[g+1]) take the
  * weight g of wq [G, N, K] and sw [G, ceil(N/128), ceil(K/128)]; rows of no
  * group are not written. offsets NULL: G must be 1 and takes all rows.
+ * The blocks of a grouped product are added in order, so a row's result does
+ * not depend on the other rows; one product alone may add them in up to 8
+ * slices, by a rule on M, N and K. A call gives the same bits every time.
  * K a multiple of 16 (any N >= 1, M >= 0), 1 <= G <= 256, M <= 2^24, N and
  * K <= 2^17, G * N < 2^31; xq, wq and out 16-byte aligned. ws: a device
  * workspace of moe_block_workspace_size bytes, 256-byte aligned, zeroed once

@@ -425,8 +425,10 @@ def moe_block_gemm(xq, sx, wq, sw, out, ws, offsets=None, stream=None) -> None:
     kb, nb = -(-K // 128), -(-N // 128)
     lead = () if offsets is None else (G,)
     if xq.shape != (M, K) or sx.shape != (M, kb) or wq.shape != lead + (N, K) or \
-            sw.shape != lead + (nb, kb) or out.shape != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
-            (offsets is not None and (offsets.numel() != G + 1 or offsets.dtype != torch.int32)) or \
+            sw.shape != lead + (nb, kb) or out.shape != (M, N) or \
+            out.dtype not in (torch.bfloat16, torch.float32) or \
+            (offsets is not None and (offsets.numel() != G + 1 or offsets.dtype != torch.int32 or
+                                      not offsets.is_contiguous())) or \
             xq.element_size() != 1 or wq.element_size() != 1 or sx.dtype != torch.float32 or \
             sw.dtype != torch.float32 or not all(t.is_contiguous() for t in (xq, sx, wq, sw, out)):
         raise MoeError("moe_block_gemm", MOE_ERR_INVALID_ARG)

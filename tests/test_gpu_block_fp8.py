@@ -6,7 +6,7 @@ import torch
 
 import block_reference as ref
 from sparse_moe_transformer_gemm_b200 import build as moe_build
-from sparse_moe_transformer_gemm_b200 import moe
+from sparse_moe_transformer_gemm_b200 import ep, moe
 
 pytestmark = pytest.mark.gpu
 
@@ -78,6 +78,40 @@ def test_quant_extremes():
     x[6, 300] = -448.0
     x[7, 0:128] = 2.0 ** torch.arange(-64, 64, device="cuda").float()
     check_quant(x.to(torch.bfloat16))
+
+
+def test_quant_of_subnormals():
+    """Blocks whose largest magnitude is a subnormal bf16 (m 2^-133, m < 128): the scale is
+    m 1024 / 7 steps of 2^-149, never halfway between two."""
+    m = torch.arange(0, 128, device="cuda").double()
+    x = torch.zeros(128, 128, device="cuda", dtype=torch.float64)
+    for r in range(128):
+        x[r] = torch.minimum(m, m[r]) * 2.0 ** -133
+    check_quant(x.to(torch.bfloat16))
+
+
+def test_quant_past_two_to_the_31_elements():
+    M, K = 131075, 16400
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    rows = torch.cat([torch.arange(0, 3), torch.randint(0, M, (60,)),
+                      torch.arange(M - 3, M)]).unique().to("cuda")
+    x[rows] = activations(gen(32), rows.numel(), K)
+    q, s = quantised(x)
+    q2, s2 = quantised(x[rows].contiguous())
+    assert torch.equal(q[rows], q2) and torch.equal(s[rows], s2)
+    assert int((s != 1).any(1).sum()) == rows.numel()
+
+
+def test_quant_in_a_graph_on_another_stream():
+    x = activations(gen(33), 70, 1536)
+    q, s = quantised(x)
+    q2, s2 = torch.zeros_like(q), torch.zeros_like(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_block_quant(x, q2, s2)
+    x.neg_()
+    graph.replay()
+    assert torch.equal(s, s2) and torch.equal(q.view(ref.FP8).float(), -q2.view(ref.FP8).float())
 
 
 def test_quant_of_infinities_and_nan_is_not_finite_in_that_block_only():
@@ -419,3 +453,83 @@ def test_layer_on_another_stream_with_its_own_workspace():
         moe.moe_forward_routed(p["cfg"], p["x"], p["idx"], p["w"], *weights, a, p["ws"])
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+# The kernels that take many, up to 128, 64 and 32 rows a group on average, by the
+# number of (empty) groups beside the one with rows.
+@pytest.mark.parametrize("M", [1, 77, 300])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_row_has_the_same_bits_in_every_grouped_kernel(M, dtype):
+    """Every kernel adds a row's blocks in order with one fused multiply-add each."""
+    g = gen(M)
+    N, K = 400, 912
+    q, s = quantised(activations(g, M, K))
+    w, v = ref.random_weight(g, N, K)
+    outs = []
+    for per_group in (200, 100, 20, 1):
+        G = max(1, -(-M // per_group))
+        if G > 256:
+            G = 256
+        if per_group == 1 and G < M:
+            continue
+        wq = torch.stack([w] + [torch.zeros_like(w)] * (G - 1))
+        sw = torch.stack([v] + [torch.ones_like(v)] * (G - 1))
+        offsets = torch.full((G + 1,), M, dtype=torch.int32, device="cuda")
+        offsets[0] = 0
+        outs.append(product(q, s, wq, sw, N, dtype, offsets))
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("counts", [[3, 5, 1, 7], [40, 33, 64, 2], [90, 100, 70, 128],
+                                    [257, 200, 130, 300]])
+def test_nan_rows_and_nan_weights_stay_in_their_group(counts):
+    """A NaN row changes no other row, NaN weights of one group no other group."""
+    g = gen(sum(counts))
+    G, N, K = len(counts), 264, 400
+    offsets = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+    M = sum(counts)
+    x = activations(g, M, K)
+    ws = [ref.random_weight(g, N, K) for _ in range(G)]
+    wq, sw = torch.stack([w for w, _ in ws]), torch.stack([v for _, v in ws])
+    q, s = quantised(x)
+    clean = product(q, s, wq, sw, N, offsets=offsets)
+    bad = offsets[1:-1].tolist() + [M - 1]  # the first row of each later group, the last row
+    x[bad] = float("nan")
+    q, s = quantised(x)
+    wq[2] = 0x7F
+    out = product(q, s, wq, sw, N, offsets=offsets)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    keep[offsets[2]:offsets[3]] = False
+    assert torch.equal(out[keep], clean[keep])
+    assert bool(torch.isnan(out[~keep]).all())
+
+
+def test_a_nan_token_leaves_the_other_tokens_alone():
+    p = make(200, 512, 16, 4, 256, 12)
+    weights = (p["wgu"], p["sgu"], p["wd"], p["sd"])
+    a, b = (torch.empty(200, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    moe.moe_forward_routed(p["cfg"], p["x"], p["idx"], p["w"], *weights, a, p["ws"])
+    p["x"][[0, 57, 199], 5] = float("nan")
+    moe.moe_forward_routed(p["cfg"], p["x"], p["idx"], p["w"], *weights, b, p["ws"])
+    keep = torch.ones(200, dtype=torch.bool, device="cuda")
+    keep[[0, 57, 199]] = False
+    assert torch.equal(a[keep], b[keep]) and bool(torch.isnan(b[~keep]).all())
+
+
+@pytest.mark.parametrize("T,P", [(64, 2), (400, 4)])
+def test_expert_parallel_ranks_equal_the_layer_on_one_gpu(T, P):
+    """Ranks in lockstep on one GPU: bitwise moe_forward on each rank's tokens."""
+    p = make(T, 512, 32, 4, 256, 13)
+    wg = (torch.randn(32, 512, device="cuda", generator=gen(14)) * 0.05).to(torch.bfloat16)
+    weights = (p["wgu"], p["sgu"], p["wd"], p["sd"])
+    part = ep.Partition(32, P)
+    ops = [ep.ep_layer_ops(p["cfg"], part, r, wg, None, *weights) for r in range(P)]
+    xs = [x.contiguous() for x in torch.chunk(p["x"], P)]
+    outs = ep.ep_forward_lockstep(ops, part, xs)
+    for x, out in zip(xs, outs):
+        cfg = moe.config(x.shape[0], 512, 32, 4, 256, fp8_block=True)
+        ws, want = moe.workspace(cfg), torch.empty_like(x)
+        moe.moe_forward(cfg, x, wg, None, *weights, want, ws)
+        assert torch.equal(out, want) and moe.moe_read_status(ws) == moe.MOE_OK

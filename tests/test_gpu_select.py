@@ -156,6 +156,16 @@ def test_strided_rows_and_untouched_neighbours():
     assert np.array_equal(idx, idx2) and np.array_equal(w, w2)
 
 
+def test_rows_past_two_to_the_31_elements():
+    """Row 5 begins 2.7e9 logits behind row 0."""
+    ld = 1 << 29
+    z = torch.empty(5 * ld + 64, device="cuda")
+    rows = torch.as_strided(z, (6, 64), (ld, 1))
+    rows.copy_(logits(6, 64, 40))
+    check(rows, 6, fn="softmax")
+    check(rows, 6, bias=bias_of(64), groups=4, keep=2, by="top2")
+
+
 def test_whole_batch_of_a_long_prefill_agrees_with_sorted_logits():
     z = logits(16384, 192, 9)
     idx, w = run(z, 8)
