@@ -5,36 +5,39 @@
 // each CTA staging 128 of them): 32 KB through shared memory per CTA and block
 // of 128 columns. A block's sums start from zero in one of two 256-column TMEM
 // accumulators, each handed over in two halves of 128 columns. A thread of the
-// promotion owns one token and 64 of the tile's columns: the block's factor
-// sx[token] sw[rows] is one register for all of them (two in gate_up), and the
-// sum of a block is one fused multiply-add per value. (With the weight rows in M
-// and the tokens in N the factors differ per column and come from shared memory,
-// 16 bytes per 4 values and thread: the product 8192 x 8192 x 4096 took 706 us
-// that way.)
+// promotion owns one token and a half's 128 columns: the block's factor
+// sx[token] sw[rows] is one register for 64 of them, and the sum of a block is one
+// fused multiply-add per value. (With the weight rows in M and the tokens in N the
+// factors differ per column and come from shared memory, 16 bytes per 4 values and
+// thread: the product 8192 x 8192 x 4096 took 706 us that way.)
 //
 // gate_up: the even CTA stages the gate rows of one 128-feature block, the odd
 // CTA its up rows; a half holds 64 features' gate columns, then their up columns.
-// A thread holds 32 gate and the same 32 up values of its token, so SiLU(g) u, the
+// A thread holds 64 gate and the same 64 up values of its token, so SiLU(g) u, the
 // token's largest |h| and the codes need no exchange but one float from each of
-// the token's four threads.
+// the token's two threads.
 //
-// What bounds it: the hand-over of the accumulators (MMA, commit, read, arrive, next
-// MMA), about 900 cycles per block against 512 of MMAs; more TMEM than there is
-// would hide it. Measured steps, product 8192 x 8192 x 4096: factors loaded by the
-// promotion itself 509 us, from a ring in shared memory 360 us; issuing warps with
-// warp-uniform control flow (the MMA warp alone had needed 1000 cycles a block), the
-// factors waited for once in 4 blocks and four promotion groups in place of two with
-// 128 columns a thread 346 us; halves with an issuing warp each 305 us; a tile
-// looked up once and waits as one short loop 282 us (1.95 PFLOP/s; 326 us after
-// a second of load, at the power cap). 128 weight rows a tile with four accumulators in
-// flight: 507 us. Tensor pipe 44% active.
+// What bounds it: the promotion's chain of a block (waits, two rounds of tcgen05.ld,
+// 128 two-value multiply-adds per scheduler), about 1000 cycles against 512 of MMAs;
+// when the accumulators are handed back within it makes no difference. Without the
+// loads from TMEM and the multiply-adds the product takes 170 us, without the multiply-adds
+// 192, without the loads from L2 240. Measured steps, product 8192 x 8192 x 4096:
+// factors loaded by the promotion itself 509 us, from a ring in shared memory 360 us;
+// issuing warps with warp-uniform control flow (the MMA warp alone had needed 1000
+// cycles a block), the factors waited for once in 4 blocks and four promotion groups in
+// place of two 346 us; halves with an issuing warp each 305 us; a tile looked up once
+// and waits as one short loop 282 us; the loop's state in vector registers, the factors
+// loaded before the wait for the accumulator, warps without tokens not told apart 252
+// us; two groups again, whose loads and multiply-adds overlap, 245 us (2.25 PFLOP/s),
+// which also spills nothing and draws less power. 128 weight rows a tile with four
+// accumulators in flight: 507 us. The next block's first loads under this one's last
+// multiply-adds: 254 us.
 //
-// Per CTA (640 threads): warp 0 TMA producer, warps 1 and 3 (even CTA) MMA issuers of
+// Per CTA (384 threads): warp 0 TMA producer, warps 1 and 3 (even CTA) MMA issuers of
 // one half each, warp 1 also TMEM owner, warp 2 the factors (a ring in shared
-// memory), warps 4-19 promotion and epilogue in four groups (one warp per 32 TMEM
-// lanes; groups 0 and 1 the first half, 2 and 3 the second). The promotion's
-// threads hold 96 values, so the first four warps hand registers over
-// (setmaxnreg). All waits are bounded.
+// memory), warps 4-11 promotion and epilogue in a group per half (one warp per 32 TMEM
+// lanes). The promotion's threads hold 192 values, so the first four warps hand
+// registers over (setmaxnreg). All waits are bounded.
 #include <type_traits>
 
 #include "block_tile.cuh"
@@ -51,17 +54,17 @@ constexpr int STAGE_BYTES = 2 * BM * BK;
 // 8192 2354 and 2398; with 4 1182 and 2340, but 2048 x 8192 x 4096 takes 90 us for 85.
 constexpr int STAGES = 5;
 constexpr int COLS = 256;              // TMEM columns per block
-constexpr int GROUPS = 4;              // promotion groups of 4 warps
-constexpr int PROMO_WARP = 4;          // the first of 16
+constexpr int GROUPS = 2;              // promotion groups of 4 warps, one per half
+constexpr int PROMO_WARP = 4;          // the first of 8
 constexpr int THREADS = 32 * (PROMO_WARP + 4 * GROUPS);
 constexpr int CH = 32;                 // columns per tcgen05.ld
 constexpr int SCALE_WARP = 2;
 constexpr int FB = 4;                  // blocks per slot of the factor ring
 constexpr int SLOTS = 2;
 constexpr int EPI_BYTES = 4 * GROUPS * 32 * 32;  // a [32 tokens][32 bytes] store tile per warp
-// registers a thread: 96 at launch; 5 * 96 = 32 + 4 * 112
-constexpr int REGS_FEW = 32, REGS_MANY = 112;
-static_assert(REGS_FEW + GROUPS * REGS_MANY == (1 + GROUPS) * 96, "no more than the launch gave");
+// registers a thread: 168 at launch; 3 * 168 = 72 + 2 * 216
+constexpr int REGS_FEW = 72, REGS_MANY = 216;
+static_assert(REGS_FEW + GROUPS * REGS_MANY == (1 + GROUPS) * 168, "no more than the launch gave");
 
 struct Ctrl {
     uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
@@ -126,7 +129,7 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             for (int i = 0; i < 2; ++i) {
                 for (int h = 0; h < 2; ++h) {
                     tc::mbar_init(&c.acc_full[i][h], 1);
-                    tc::mbar_init(&c.acc_empty[i][h], 2 * 4 * GROUPS / 2);
+                    tc::mbar_init(&c.acc_empty[i][h], 2 * 4);
                 }
             }
             for (int i = 0; i < SLOTS; ++i) {
@@ -152,92 +155,106 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     if (warp >= PROMO_WARP) {
         tc::regs_inc<REGS_MANY>();
         // ---------------- promotion and epilogue: lane = one token of this CTA's
-        const int quad = warp & 3, grp = (warp - PROMO_WARP) >> 2;
+        // and the 128 columns of one half: 64 of the even CTA's weight rows, 64 of the odd's
+        const int quad = warp & 3, half = (warp - PROMO_WARP) >> 2;
         const int row = quad * 32 + lane;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quad * 32) << 16);
-        const int half = grp >> 1, side = grp & 1;
-        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0][half]), 0);
-        // the two chunks of this thread's columns (half h of them: the h-th 64 rows of
-        // the even CTA's weights, then of the odd one's): gate_up 32 gate columns and
-        // their up ones, else 64 columns of one CTA's rows
-        const uint32_t col0 = half * 128 + side * (GATE_UP ? CH : 2 * CH);
-        const uint32_t col1 = col0 + (GATE_UP ? 2 * CH : CH);
         const int nb_n = (a.N + 127) / 128;
-        uint32_t blk = 0, batch = 0;
+        const uint32_t tcol = tmem_base + ((uint32_t)(quad * 32) << 16) + half * 128;
+        const uint32_t acc_full0 = tc::smem_u32(&c.acc_full[0][half]);
+        const uint32_t acc_empty0 = tc::map_to_cta(tc::smem_u32(&c.acc_empty[0][half]), 0);
+        const uint32_t sc_full0 = tc::smem_u32(&c.sc_full[0]);
+        const uint32_t sc_empty0 = tc::smem_u32(&c.sc_empty[0]);
+        const uint32_t fac0 = tc::smem_u32(&c.factor[0][0][0][row]);
+        // The loop's state in bytes, and in vector registers: kept as block counts the
+        // compiler puts it and all that follows from it on the uniform path, 40
+        // instructions a block and warp more and 7% of the kernel's time.
+        constexpr uint32_t SLOT_BYTES = sizeof(c.factor[0]);
+        uint32_t buf = 0, par = 0;        // 16 x the accumulator, its phase
+        uint32_t fac_at = 0, sc_par = 0;  // the block's place in the ring of factors, its phase
         for (int t = pair, i_t = 0; t < total; t += n_pairs, ++i_t) {
             const Tile ti = listed_tile<NM>(c.list, c.tab, a.G, i_t, t);
-            const int tok = rank * BM + row;                     // token within the tile
+            const int tok = rank * BM + row;  // token within the tile
             const bool mine = tok < ti.len;
-            const bool active = rank * BM + quad * 32 < ti.len;  // any token of the warp
-            uint64_t acc[2][CH / 2];
+            uint64_t acc[4][CH / 2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < CH / 2; ++j) acc[i][j] = 0;
             bool ok = true;
-            for (int kb = 0; kb < KB; ++kb, ++blk) {
-                const uint32_t as = blk & 1u, slot = batch % SLOTS;
-                if (kb % FB == 0)
-                    ok = tc::mbar_wait_warp(&c.sc_full[slot], (batch / SLOTS) & 1u, abort_flag);
-                ok = ok && tc::mbar_wait_warp(&c.acc_full[as][half], (blk >> 1) & 1u, abort_flag);
+            for (int kb = 0; kb < KB; ++kb) {
+                if (fac_at % SLOT_BYTES == 0)
+                    ok = tc::mbar_wait_warp_at(sc_full0 + fac_at / SLOT_BYTES * 8, sc_par, abort_flag);
+                const float f0 = tc::ld_shared_f32(fac0 + fac_at);
+                const float f1 = tc::ld_shared_f32(fac0 + 4 * BM + fac_at);
+                ok = tc::mbar_wait_warp_at(acc_full0 + buf, par, abort_flag) && ok;
                 if (!ok) break;
-                float f0 = 0.f, f1 = 0.f;
-                uint32_t d[CH];
-                if (active) {
-                    tc::fence_after_sync();
-                    const uint32_t tb = lane_base + as * COLS;
-                    tc::tmem_ld32(tb + col0, d);
-                    f0 = c.factor[slot][kb % FB][GATE_UP ? 0 : side][row];
-                    f1 = GATE_UP ? c.factor[slot][kb % FB][1][row] : f0;
-                    tc::tmem_ld_wait();
-                    tc::tmem_loaded(d);
-                    promote(acc[0], d, f0);
-                    tc::tmem_ld32(tb + col1, d);
-                    tc::tmem_ld_wait();
-                    tc::tmem_loaded(d);
-                }
-                const bool last = kb % FB == FB - 1 || kb + 1 == KB;
+                tc::fence_after_sync();
+                const uint32_t tb = tcol + buf * (COLS / 16);
+                uint32_t d0[CH], d1[CH];
+                tc::tmem_ld32(tb, d0);
+                tc::tmem_ld32(tb + CH, d1);
+                tc::tmem_ld_wait();
+                tc::tmem_loaded(d0);
+                tc::tmem_loaded(d1);
+                promote(acc[0], d0, f0);
+                tc::tmem_ld32(tb + 2 * CH, d0);
+                promote(acc[1], d1, f0);
+                tc::tmem_ld32(tb + 3 * CH, d1);
+                tc::tmem_ld_wait();
+                tc::tmem_loaded(d0);
+                tc::tmem_loaded(d1);
                 tc::fence_before_sync();
-                if (tc::elect_one()) {
-                    tc::mbar_arrive_cluster_read(acc_empty0 + as * 16);
-                    if (last) tc::mbar_arrive(&c.sc_empty[slot]);
-                }
+                if (tc::elect_one()) tc::mbar_arrive_cluster_read(acc_empty0 + buf);
                 __syncwarp();
-                batch += last;
-                if (active) promote(acc[1], d, f1);
+                par ^= buf >> 4;
+                buf ^= 16;
+                fac_at += 2 * BM * 4;
+                if (fac_at % SLOT_BYTES == 0 || kb + 1 == KB) {
+                    if (lane == 0) tc::mbar_arrive_at(sc_empty0 + (fac_at - 1) / SLOT_BYTES * 8);
+                    fac_at = (fac_at + SLOT_BYTES - 1) / SLOT_BYTES % SLOTS * SLOT_BYTES;
+                    sc_par ^= fac_at == 0;
+                }
+                tc::opaque(buf);
+                tc::opaque(par);
+                tc::opaque(fac_at);
+                tc::opaque(sc_par);
+                promote(acc[2], d0, f1);
+                promote(acc[3], d1, f1);
             }
             if constexpr (GATE_UP) {
-                // h in acc[0]; the token's largest |h| over all groups' columns
+                // h in acc[0] and acc[1]; the token's largest |h| over both groups' columns
                 uint32_t mx = 0;
 #pragma unroll
-                for (int j = 0; j < CH; j += 2) {
-                    const float h0 = silu_mul(value_at(acc[0], j), value_at(acc[1], j));
-                    const float h1 = silu_mul(value_at(acc[0], j + 1), value_at(acc[1], j + 1));
-                    acc[0][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
-                    mx = max(mx, max(f32_bits(h0) & 0x7FFFFFFFu, f32_bits(h1) & 0x7FFFFFFFu));
-                }
-                c.amax[grp][row] = f32_from_bits(mx);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < CH; j += 2) {
+                        const float h0 = silu_mul(value_at(acc[i], j), value_at(acc[i + 2], j));
+                        const float h1 =
+                            silu_mul(value_at(acc[i], j + 1), value_at(acc[i + 2], j + 1));
+                        acc[i][j / 2] = pack2(f32_bits(h0), f32_bits(h1));
+                        mx = max(mx, max(f32_bits(h0) & 0x7FFFFFFFu, f32_bits(h1) & 0x7FFFFFFFu));
+                    }
+                c.amax[half][row] = f32_from_bits(mx);
                 // (a warp that gave up takes the others with it)
                 if (tc::bar_any(1, 128 * GROUPS, !ok)) {
                     give_up(c, a.status);
                     break;
                 }
                 const BlockScale b = block_scale(f32_from_bits(
-                    max(max(f32_bits(c.amax[0][row]), f32_bits(c.amax[1][row])),
-                        max(f32_bits(c.amax[2][row]), f32_bits(c.amax[3][row])))));
+                    max(f32_bits(c.amax[0][row]), f32_bits(c.amax[1][row]))));
                 const BlockScale2 b2 = twice(b);
                 if (mine) {
                     const long r = ti.row0 + tok;
-                    if (grp == 0) a.out_scales[r * nb_n + ti.m] = b.scale;
+                    if (half == 0) a.out_scales[r * nb_n + ti.m] = b.scale;
                     uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + r * a.N +
-                                                        ti.m * 128 + grp * CH);
+                                                        ti.m * 128 + half * 2 * CH);
 #pragma unroll
-                    for (int q = 0; q < CH / 16; ++q) {
+                    for (int q = 0; q < 2 * CH / 16; ++q) {
                         uint32_t w[4];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) {
-                            const int j = q * 16 + v * 4;
-                            const auto& h = acc[0];
+                            const int j = (q & 1) * 16 + v * 4;
+                            const auto& h = acc[q >> 1];
                             const float2 q0 =
                                 block_quotient2(b2, value_at(h, j), value_at(h, j + 1));
                             const float2 q1 =
@@ -253,9 +270,8 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     give_up(c, a.status);
                     break;
                 }
-                if (!active) continue;
-                const int n0 = ti.m * COLS + side * 128 + half * 2 * CH;  // first output column
-                const int rows = ti.len - rank * BM - quad * 32; // tokens of this warp
+                if (rank * BM + quad * 32 >= ti.len) continue;  // no token of this warp
+                const int rows = ti.len - rank * BM - quad * 32;  // tokens of this warp
                 const long r0 = ti.row0 + rank * BM + quad * 32;
                 // EC columns at a time through the warp's [32 tokens][32 bytes] tile, its
                 // 16-byte halves swapped for every other four tokens (no bank conflicts):
@@ -266,7 +282,9 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 uint4* st = reinterpret_cast<uint4*>(
                     epi + (warp - PROMO_WARP) * (EPI_BYTES / (4 * GROUPS)));
 #pragma unroll
-                for (int i = 0; i < 2 * CH / EC; ++i) {
+                for (int i = 0; i < 4 * CH / EC; ++i) {
+                    // first output column: 64 of the even CTA's rows, then of the odd one's
+                    const int n0 = ti.m * COLS + half * 64 + i * EC / 64 * 128 + i * EC % 64;
                     __syncwarp();  // the previous pass is read
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
@@ -285,12 +303,12 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         st[lane * 2 + (q ^ ((lane >> 2) & 1))] = u;
                     }
                     __syncwarp();
-                    Out* o = static_cast<Out*>(a.out) + r0 * a.N + n0 + i * EC;
+                    Out* o = static_cast<Out*>(a.out) + r0 * a.N + n0;
                     if (vec) {
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
                             const int n = q * 16 + (lane >> 1), ch = lane & 1;
-                            if (n < rows && n0 + i * EC + ch * PIECE < a.N)
+                            if (n < rows && n0 + ch * PIECE < a.N)
                                 *reinterpret_cast<uint4*>(o + (long)n * a.N + ch * PIECE) =
                                     st[n * 2 + (ch ^ ((n >> 2) & 1))];
                         }
@@ -299,7 +317,7 @@ block_many_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 #pragma unroll 1
                         for (int e = lane; e < 32 * EC; e += 32) {
                             const int n = e / EC, c0 = e % EC, ch = c0 / PIECE;
-                            if (n < rows && n0 + i * EC + c0 < a.N)
+                            if (n < rows && n0 + c0 < a.N)
                                 o[(long)n * a.N + c0] = reinterpret_cast<const Out*>(
                                     st + n * 2 + (ch ^ ((n >> 2) & 1)))[c0 % PIECE];
                         }

@@ -62,16 +62,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// (addr: the barrier's shared-memory address)
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t addr, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(addr), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait_at(smem_u32(bar), parity);
 }
 
 // Wait until the phase of parity `parity` has completed. Returns false if the
@@ -99,12 +108,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // loop is one rolled one (the compiler unrolls a counted loop of tries; a kernel
 // whose roles' loops do not fit the instruction cache together loses a factor of
 // two).
-__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
-                                              const volatile int* abort_flag) {
+__device__ __forceinline__ bool mbar_wait_hot_at(uint32_t addr, uint32_t parity,
+                                                 const volatile int* abort_flag) {
     uint64_t t0 = 0;
 #pragma unroll 1
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try_wait_at(addr, parity)) return true;
         if ((i & 1023u) == 0u) {
             const uint64_t now = globaltimer_ns();
             if (*abort_flag || (t0 && now - t0 > kWaitNs)) return false;
@@ -113,11 +122,29 @@ __device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
     }
 }
 
+__device__ __forceinline__ bool mbar_wait_hot(uint64_t* bar, uint32_t parity,
+                                              const volatile int* abort_flag) {
+    return mbar_wait_hot_at(smem_u32(bar), parity, abort_flag);
+}
+
 // mbar_wait_hot by a converged warp: all lanes get the same answer.
+__device__ __forceinline__ bool mbar_wait_warp_at(uint32_t addr, uint32_t parity,
+                                                  const volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait_hot_at(addr, parity, abort_flag));
+}
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
                                                const volatile int* abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait_hot(bar, parity, abort_flag));
 }
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The compiler knows nothing of x from here on (not that the warp's lanes agree on it).
+__device__ __forceinline__ void opaque(uint32_t& x) { asm volatile("" : "+r"(x)); }
 
 // ------------------------------------------------------------------ TMA
 
