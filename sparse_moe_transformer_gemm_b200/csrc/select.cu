@@ -11,14 +11,17 @@
 // with the logit, so without a bias the experts are ranked by the logits
 // themselves; with one, and for sums of two scores, by fp32 evaluations. A token's
 // common path is choose_packed on 32-bit keys. Where a comparison that decides
-// something is closer than the bits cut off or the evaluation's error, the token
-// is chosen once more exactly, with scores in fp64: about one token in 500 with a
-// bias, one in 50000 without.
+// something is closer than the bits cut off or the evaluation's error, the candidates
+// are put in order by one fp64 evaluation a lane (order_exactly); where it is a group
+// that is open, or the candidates themselves, the whole token is chosen once more with
+// scores in fp64 (select_exactly, about 7 us for a token by itself). With a bias that
+// is about one token in 500 together, without one in 50000.
 //
-// Bound: about 450 instructions per token against 4 E bytes read. Measured, E =
-// 256, top-8, T = 16384: 13.3 us without a bias or groups (reading the logits
-// takes 2.6); biased, 4 of 8 groups by their two best: 30 us, of which about 7
-// are the latency of the few exact tokens. T = 64: 2.8 us, the launch's.
+// Bound: about 600 instructions per token against 4 E bytes read. Measured, E =
+// 256, top-8, T = 16384: 13.5 us without a bias or groups (reading the logits
+// takes 2.6); biased, E = 192 17.6 us; biased, 4 of 8 groups by their two best 25.8
+// us, of which 4 are the latency of tokens with an open group (30 before the
+// candidates had an order of their own). T = 64: 2.8 us, the launch's.
 #include <float.h>
 
 #include "common.cuh"
@@ -30,7 +33,7 @@ namespace {
 constexpr int WARPS = 4;      // tokens per CTA
 constexpr int Q = 8;          // experts per lane
 constexpr int PAD_E = 256 + 8;
-constexpr int kCtasPerSm = 8;  // persistent CTAs
+constexpr int kCtasPerSm = 7;  // persistent CTAs: 8 spill registers, 6 leave issue slots
 
 struct SelectArgs {
     const float* logits;
@@ -218,15 +221,24 @@ __device__ __forceinline__ void choose(const SelectArgs& a, const float (&z)[Q],
 // upper 29 bits of the value's order-preserving key, then 7 - q for the lane's
 // q-th expert (of equal values the earlier one first). Each lane sorts its 8 keys
 // once (19 compare-exchanges); a round is one redux.sync on the lanes' heads and a
-// ballot. Values whose difference is within the cut-off bits or the evaluation's
-// error make the result void (false, uniform): the caller repeats the token
-// exactly. `mine`: 8 * lane + q of this lane's choice.
+// ballot. `mine`: 8 * lane + q of lane j's j-th expert, 0 <= j <= k (`exists`: there
+// is one; lane k has the first that was left out). Values whose difference is
+// within the cut-off bits or the evaluation's error leave their order open: kOrder
+// if it is only that of these k + 1, kOpen if the k + 2nd may belong among them.
+enum Certainty { kSure, kOrder, kOpen };
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
     const uint32_t hi = max(a, b), lo = min(a, b);
     a = hi;
     b = lo;
 }
-__device__ __forceinline__ bool choose_packed(uint32_t (&h)[Q], int k, float error, int& mine) {
+__device__ __forceinline__ bool sure_order(uint32_t key, uint32_t next, float error) {
+    if (error == 0.f || next == 0) return (key ^ next) > 7u;  // different after the cut
+    const float v = key_value(key & ~7u), u = key_value(next & ~7u);
+    const float big = fmaxf(fabsf(v), fabsf(u));
+    return v - u > fmaf(1e-6f, big, error * (1.0f + big));  // (false for two -infinities)
+}
+__device__ __forceinline__ Certainty choose_packed(uint32_t (&h)[Q], int k, float error, int& mine,
+                                                   bool& exists) {
     const int lane = threadIdx.x & 31;
     // a sorting network of 8 (Batcher's odd-even merge), descending
     exchange(h[0], h[1]); exchange(h[2], h[3]); exchange(h[4], h[5]); exchange(h[6], h[7]);
@@ -253,13 +265,41 @@ __device__ __forceinline__ bool choose_packed(uint32_t (&h)[Q], int k, float err
     // lane j: its choice against the next one (or the first one left out; 0: none is)
     uint32_t next = __shfl_down_sync(0xffffffffu, key, 1);
     if (lane == k - 1) next = left_out;
-    bool sure = (key ^ next) > 7u;  // different keys after the cut are in order
-    if (error > 0.f && next != 0) {
-        const float v = key_value(key & ~7u), u = key_value(next & ~7u);
-        const float big = fmaxf(fabsf(v), fabsf(u));
-        sure = v - u > fmaf(1e-6f, big, error * (1.0f + big));  // (false for two -infinities)
+    exists = lane <= k && key != 0;
+    if (__all_sync(0xffffffffu, lane >= k || sure_order(key, next, error))) return kSure;
+    const uint32_t after = __reduce_max_sync(0xffffffffu, h[0]);
+    const bool closed = left_out == 0 || after == 0 || sure_order(left_out, after, error);
+    return closed && k < 32 ? kOrder : kOpen;
+}
+
+// The exact order of a token's k + 1 candidates (lane j: expert e, if `exists`), one
+// evaluation in fp64 a lane: lane j gets the j-th. Not for the softmax, whose sum
+// takes all experts. Out of line, as the whole token's repeat is.
+__device__ __noinline__ int order_exactly(const SelectArgs& a, const float* row, int e,
+                                          bool exists) {
+    const int lane = threadIdx.x & 31;
+    double v = -INFINITY;
+    if (exists) {
+        const float z = cleaned(row[e]);
+        v = z;
+        if (a.bias && z > -INFINITY) v = score_of(v, a.score_fn) + (double)cleaned(a.bias[e]);
+    } else {
+        e = 256;  // behind every expert
     }
-    return __all_sync(0xffffffffu, sure || lane >= k);
+    int rank = 0;
+#pragma unroll 1
+    for (int i = 0; i <= a.k; ++i) {
+        const double u = __shfl_sync(0xffffffffu, v, i);
+        const int f = __shfl_sync(0xffffffffu, e, i);
+        rank += u > v || (u == v && f < e);
+    }
+    int mine = 0;
+#pragma unroll 1
+    for (int i = 0; i <= a.k; ++i) {
+        const int f = __shfl_sync(0xffffffffu, e, i);
+        if (__shfl_sync(0xffffffffu, rank, i) == lane) mine = f;
+    }
+    return mine;
 }
 
 // Lane j < k: the weight of its expert from that expert's logit zj; z and zmax (the
@@ -418,14 +458,16 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
                            ? (order_key(top2 && !a.bias ? z[q] : c[q]) & ~7u) | (uint32_t)(7 - q)
                            : 0u;
             int e = 0;
-            if (!choose_packed(h, a.k, a.bias ? kScoreError : 0.f, e)) sure = false;
-            if (!sure) {
+            bool candidate;
+            const Certainty order = choose_packed(h, a.k, a.bias ? kScoreError : 0.f, e, candidate);
+            if (!sure || order == kOpen || (order == kOrder && FN == MOE_SCORE_SOFTMAX)) {
                 open |= 1ull << i;
                 continue;
             }
             const int l = e >> 3, q = e & 7;
             e = GROUPS ? (l >> shift) * n + (l & (lanes - 1)) * Q + q : l + 32 * q;
             const float* row = a.logits + t * a.ld;
+            if (order == kOrder) e = order_exactly(a, row, e, candidate);
             const float w =
                 weight_of(a, FN, z, zmax, lane < a.k ? cleaned(row[e]) : -INFINITY);
             if (lane < a.k) {

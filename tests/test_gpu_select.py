@@ -130,6 +130,26 @@ def test_values_closer_than_fp32_resolves_keep_the_exact_order():
 
 
 @pytest.mark.parametrize("fn", ["sigmoid", "sqrtsoftplus", "softmax"])
+@pytest.mark.parametrize("k", [1, 2, 7, 8, 31, 32])
+def test_pairs_closer_than_fp32_resolves_keep_the_exact_order(fn, k):
+    """Pairs of experts whose choice values are within 1e-7 of each other and 0.02 from
+    the next pair's: within the choice (k even) and across its border (k odd); rows
+    0 to 9 have equal logits in a pair with equal biases."""
+    E = 80
+    z = logits(1, E, 13).repeat(200, 1)
+    z[:, 1:20:2] = z[:, 0:20:2]
+    s = (ref.score64(z.cpu().numpy()[0], fn) if fn != "softmax"
+         else torch.softmax(z[0].double(), 0).cpu().numpy())
+    pair = np.random.default_rng(3).permutation(E // 2).repeat(2)
+    b = torch.tensor((0.02 * pair - s).astype(np.float32), device="cuda")
+    z[10:] += logits(190, E, 14, 1e-7)
+    check(z, k, fn=fn, bias=b)
+    if k <= 10:
+        check(z, k, fn=fn, bias=b, groups=8, keep=3, by="top2")
+        check(z, k, fn=fn, bias=b, groups=8, keep=5, by="max", renorm=False)
+
+
+@pytest.mark.parametrize("fn", ["sigmoid", "sqrtsoftplus", "softmax"])
 def test_very_small_scores_renormalise(fn):
     z = logits(20, 40, 5) - 300.0
     check(z, 6, fn=fn)
