@@ -70,6 +70,9 @@ __device__ __forceinline__ void promote(uint64_t (&acc)[CH / 2], const uint32_t 
     }
 }
 
+// Token maps in use: tiles hold up to 16, 32 or 128 rows.
+__host__ __device__ constexpr int boxes(int M, int NT) { return M <= 16 ? 1 : NT == 32 ? 2 : 4; }
+
 // grid (row tiles, token tiles, S), clusters (1, 1, S). tmA: weights [N, K] bytes, box
 // 128 x 128; tmB: tokens [M, K] bytes.
 template <int NT, bool OUT_F32>
@@ -93,7 +96,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         if (lane == 0) {
             c.abort = 0;
             tc::prefetch_tensormap(&tmA);
-            for (int m = 0; m < 4; ++m) tc::prefetch_tensormap(&tmB.m[m]);
+            for (int m = 0; m < boxes(a.M, NT); ++m) tc::prefetch_tensormap(&tmB.m[m]);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -336,7 +339,8 @@ cudaError_t launch(const BlockGemm& p, int S, cudaStream_t s) {
                     nullptr, 0};
     CUtensorMap ma;
     TokenMaps mb;
-    if (!make_byte_map(&ma, p.wq, p.N, p.K, BM) || !make_token_byte_maps(&mb, p.xq, p.M, p.K, p.M <= 16 ? 1 : NT == 32 ? 2 : 4))
+    if (!make_byte_map(&ma, p.wq, p.N, p.K, BM) ||
+        !make_token_byte_maps(&mb, p.xq, p.M, p.K, boxes(p.M, NT)))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     auto kernel = block_split_kernel<NT, OUT_F32>;
