@@ -80,7 +80,7 @@ __device__ __forceinline__ double warp_total(double v) {
 // slope s (1 - s) turns into at most 8e-8, the fast reciprocal adds 2 ulp, the sum
 // with the bias half of one: together below 4e-7 of 1 + |c|; the softmax's sum and
 // the sqrt-softplus stay below that too. The difference of two of them is
-// certain beyond kScoreError of 1 + |c|, that of two sums beyond twice as much.
+// certain beyond kScoreError of 1 + |c|.
 constexpr float kScoreError = 1e-6f;
 __device__ __forceinline__ float score_of(float z, int fn) {
     if (fn == MOE_SCORE_SOFTMAX) return __expf(z);
@@ -93,10 +93,13 @@ __device__ __forceinline__ double score_of(double z, int fn) {
     return 1.0 / (1.0 + exp(-z));
 }
 
-// Whether a > b can be told apart in spite of the evaluation's error (of sums of
-// two scores; a tie of two -infinities is decided by the index).
-__device__ __forceinline__ bool decided(float a, float b) {
-    return b == -INFINITY || a - b > 2 * kScoreError * (1.0f + fmaxf(fabsf(a), fabsf(b)));
+// How far a group's score, the largest value v1 (v2 = 0) or the sum v1 + v2,
+// may be from its exact value: each term's error goes with its own magnitude, which
+// the sum's may be far below (large biases of opposite signs). Two evaluations, 8e-7 +
+// 4e-7 (|v1| + |v2|), and the sum's rounding and this bound's stay below it. A group
+// without enough experts left has -infinity, exactly; sums that overflow stay open.
+__device__ __forceinline__ float group_error(float v1, float v2) {
+    return fminf(v1, v2) == -INFINITY ? 0.f : kScoreError * (1.0f + fabsf(v1) + fabsf(v2));
 }
 
 template <typename V>
@@ -444,11 +447,16 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
                 }
                 kept = ahead < a.topk_group;
                 if (evaluated && a.topk_group < a.n_group) {
-                    const uint32_t key = order_key(own);
+                    // the least a kept group may be worth against the most another may
+                    // (two -infinities: the index decides)
                     const bool is = group < a.n_group;
-                    sure = decided(
-                        key_value(__reduce_min_sync(0xffffffffu, kept && is ? key : ~0u)),
-                        key_value(__reduce_max_sync(0xffffffffu, kept || !is ? 0u : key)));
+                    const float error = group_error(v1, top2 ? v2 : 0.f);
+                    const float least = own == -INFINITY ? own : fmaxf(own - error, -FLT_MAX);
+                    const float low = key_value(
+                        __reduce_min_sync(0xffffffffu, kept && is ? order_key(least) : ~0u));
+                    const uint32_t high =
+                        __reduce_max_sync(0xffffffffu, kept || !is ? 0u : order_key(own + error));
+                    sure = key_value(high) == -INFINITY || low > key_value(high);
                 }
             }
             uint32_t h[Q];
