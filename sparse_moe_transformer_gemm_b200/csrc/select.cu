@@ -78,10 +78,15 @@ __device__ __forceinline__ double warp_total(double v) {
 // The fp32 scores (softmax: before the division by the sum; z - max for z). The
 // fast exponential is within |z| 2^-24 + 2^-22 of its value, which the sigmoid's
 // slope s (1 - s) turns into at most 8e-8, the fast reciprocal adds 2 ulp, the sum
-// with the bias half of one: together below 4e-7 of 1 + |c|; the softmax's sum and
-// the sqrt-softplus stay below that too. The difference of two of them is
-// certain beyond kScoreError of 1 + |c|.
+// with the bias half of one: together below 4e-7 of 1 + |c|, and the softmax's sum
+// stays below that too. The sqrt-softplus is not bounded by 1: an error of 2e-7 of it
+// remains where a bias cancels it, so that `unit`, 1 or a token's largest score to
+// within 15%, takes the 1's place. The difference of two values is certain beyond
+// kScoreError of unit + |c|.
 constexpr float kScoreError = 1e-6f;
+__device__ __forceinline__ float unit_of(int fn, float zmax) {
+    return fn == MOE_SCORE_SQRT_SOFTPLUS ? sqrtf(fmaxf(zmax, 1.f)) : 1.f;
+}
 __device__ __forceinline__ float score_of(float z, int fn) {
     if (fn == MOE_SCORE_SOFTMAX) return __expf(z);
     if (fn == MOE_SCORE_SQRT_SOFTPLUS)
@@ -95,11 +100,11 @@ __device__ __forceinline__ double score_of(double z, int fn) {
 
 // How far a group's score, the largest value v1 (v2 = 0) or the sum v1 + v2,
 // may be from its exact value: each term's error goes with its own magnitude, which
-// the sum's may be far below (large biases of opposite signs). Two evaluations, 8e-7 +
+// the sum's may be far below (large biases of opposite signs). Two evaluations, 8e-7 unit +
 // 4e-7 (|v1| + |v2|), and the sum's rounding and this bound's stay below it. A group
 // without enough experts left has -infinity, exactly; sums that overflow stay open.
-__device__ __forceinline__ float group_error(float v1, float v2) {
-    return fminf(v1, v2) == -INFINITY ? 0.f : kScoreError * (1.0f + fabsf(v1) + fabsf(v2));
+__device__ __forceinline__ float group_error(float unit, float v1, float v2) {
+    return fminf(v1, v2) == -INFINITY ? 0.f : kScoreError * (unit + fabsf(v1) + fabsf(v2));
 }
 
 template <typename V>
@@ -226,7 +231,8 @@ __device__ __forceinline__ void choose(const SelectArgs& a, const float (&z)[Q],
 // once (19 compare-exchanges); a round is one redux.sync on the lanes' heads and a
 // ballot. `mine`: 8 * lane + q of lane j's j-th expert, 0 <= j <= k (`exists`: there
 // is one; lane k has the first that was left out). Values whose difference is
-// within the cut-off bits or the evaluation's error leave their order open: kOrder
+// within the cut-off bits or the evaluation's error (`error` and 1e-6 of them; 0:
+// none was evaluated) leave their order open: kOrder
 // if it is only that of these k + 1, kOpen if the k + 2nd may belong among them.
 enum Certainty { kSure, kOrder, kOpen };
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
@@ -238,7 +244,7 @@ __device__ __forceinline__ bool sure_order(uint32_t key, uint32_t next, float er
     if (error == 0.f || next == 0) return (key ^ next) > 7u;  // different after the cut
     const float v = key_value(key & ~7u), u = key_value(next & ~7u);
     const float big = fmaxf(fabsf(v), fabsf(u));
-    return v - u > fmaf(1e-6f, big, error * (1.0f + big));  // (false for two -infinities)
+    return v - u > fmaf(1e-6f + kScoreError, big, error);  // (false for two -infinities)
 }
 __device__ __forceinline__ Certainty choose_packed(uint32_t (&h)[Q], int k, float error, int& mine,
                                                    bool& exists) {
@@ -405,7 +411,10 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) z[q] = cleaned(coming[q]);
             if (t + step < a.T) load(t + step);
-            const float zmax = FN == MOE_SCORE_SOFTMAX ? largest(z) : 0.f;
+            const float zmax = FN == MOE_SCORE_SOFTMAX ||
+                                       (FN == MOE_SCORE_SQRT_SOFTPLUS && evaluated)
+                                   ? largest(z) : 0.f;
+            const float unit = unit_of(FN, zmax);
             // what experts are ranked by, and what groups sum
             float c[Q];
 #pragma unroll
@@ -450,7 +459,7 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
                     // the least a kept group may be worth against the most another may
                     // (two -infinities: the index decides)
                     const bool is = group < a.n_group;
-                    const float error = group_error(v1, top2 ? v2 : 0.f);
+                    const float error = group_error(unit, v1, top2 ? v2 : 0.f);
                     const float least = own == -INFINITY ? own : fmaxf(own - error, -FLT_MAX);
                     const float low = key_value(
                         __reduce_min_sync(0xffffffffu, kept && is ? order_key(least) : ~0u));
@@ -467,7 +476,8 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
                            : 0u;
             int e = 0;
             bool candidate;
-            const Certainty order = choose_packed(h, a.k, a.bias ? kScoreError : 0.f, e, candidate);
+            const Certainty order =
+                choose_packed(h, a.k, a.bias ? kScoreError * unit : 0.f, e, candidate);
             if (!sure || order == kOpen || (order == kOrder && FN == MOE_SCORE_SOFTMAX)) {
                 open |= 1ull << i;
                 continue;
