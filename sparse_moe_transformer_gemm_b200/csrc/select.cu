@@ -15,7 +15,10 @@
 // are put in order by one fp64 evaluation a lane (order_exactly); where it is a group
 // that is open, or the candidates themselves, the whole token is chosen once more with
 // scores in fp64 (select_exactly, about 7 us for a token by itself). With a bias that
-// is about one token in 500 together, without one in 50000.
+// is about one token in 500 together, without one in 50000, if the logits are fp32
+// sums; logits of bf16 precision have equal values among the best nine of 256 in two
+// tokens of five, which the order of the candidates settles: T = 16384 without a bias
+// 13.0 us and 20.1, the softmax 13.4 and 20.6 (28.4 where it repeated whole tokens).
 //
 // Bound: about 600 instructions per token against 4 E bytes read. Measured, E =
 // 256, top-8, T = 16384: 13.5 us without a bias or groups (reading the logits
@@ -282,7 +285,7 @@ __device__ __forceinline__ Certainty choose_packed(uint32_t (&h)[Q], int k, floa
 }
 
 // The exact order of a token's k + 1 candidates (lane j: expert e, if `exists`), one
-// evaluation in fp64 a lane: lane j gets the j-th. Not for the softmax, whose sum
+// evaluation in fp64 a lane: lane j gets the j-th. Not for a biased softmax, whose sum
 // takes all experts. Out of line, as the whole token's repeat is.
 __device__ __noinline__ int order_exactly(const SelectArgs& a, const float* row, int e,
                                           bool exists) {
@@ -478,7 +481,8 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
             bool candidate;
             const Certainty order =
                 choose_packed(h, a.k, a.bias ? kScoreError * unit : 0.f, e, candidate);
-            if (!sure || order == kOpen || (order == kOrder && FN == MOE_SCORE_SOFTMAX)) {
+            if (!sure || order == kOpen ||
+                (order == kOrder && FN == MOE_SCORE_SOFTMAX && a.bias)) {
                 open |= 1ull << i;
                 continue;
             }
