@@ -332,16 +332,22 @@ class CudaOps:
 
 def local_expert_weights(part: Partition, rank: int, w_gate_up, w_down, s_gate_up=None,
                          s_down=None):
-    """The slices of the experts' weights (and FP8 scales) that rank holds."""
+    """The slices of the experts' weights (and FP8 scales) that rank holds: views, or
+    copies where a slice (block-FP8 scales, of which an expert may have one) is not
+    16-byte aligned, as the library wants it."""
     sl = slice(rank * part.E_local, (rank + 1) * part.E_local)
-    pick = (lambda t: None if t is None else t[sl])  # noqa: E731
+
+    def pick(t):
+        t = None if t is None else t[sl]
+        return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
     return pick(w_gate_up), pick(s_gate_up), pick(w_down), pick(s_down)
 
 
 def ep_layer_ops(cfg, part: Partition, rank: int, w_gate, gate_bias, w_gate_up, s_gate_up,
                  w_down, s_down, route_options=None, stream=None) -> CudaOps:
     """CudaOps for rank ``rank`` from the full layer's tensors (the rank keeps
-    views of its experts' slices)."""
+    local_expert_weights' slices)."""
     gu, sgu, dn, sdn = local_expert_weights(part, rank, w_gate_up, w_down, s_gate_up, s_down)
     return CudaOps(cfg, part, w_gate, gate_bias, gu, sgu, dn, sdn, route_options, stream)
 
