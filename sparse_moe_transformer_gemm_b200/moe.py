@@ -362,16 +362,37 @@ def _rows(fn: str, t: torch.Tensor, rows: int, cols: int) -> int:
     return t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
+def _take(fn: str, t: Optional[torch.Tensor], dtype: torch.dtype, n: int) -> None:
+    """Refuse a tensor that is not n (or more) contiguous elements of dtype."""
+    if t is None or t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+
+
+def _take_routing(fn: str, cfg, topk_idx, topk_w) -> None:
+    _take(fn, topk_idx, torch.int32, cfg.T * cfg.k)
+    _take(fn, topk_w, torch.float32, cfg.T * cfg.k)
+
+
+def _take_router(fn: str, cfg, x, w_gate, gate_bias) -> None:
+    _take(fn, x, torch.bfloat16, cfg.T * cfg.d)
+    _take(fn, w_gate, torch.bfloat16, cfg.E * cfg.d)
+    if gate_bias is not None:
+        _take(fn, gate_bias, torch.float32, cfg.E)
+
+
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
     if logits.dtype != torch.float32:
         raise MoeError("moe_select", MOE_ERR_INVALID_ARG)
+    _take_routing("moe_select", cfg, topk_idx, topk_w)
     _check("moe_select", lib().moe_select(ctypes.byref(cfg), _p(logits),
                                           _rows("moe_select", logits, cfg.T, cfg.E), _opt(opt),
                                           _opt(grp), _p(topk_idx), _p(topk_w), _s(stream)))
 
 
 def moe_route4(cfg, x, w_gate, gate_bias, opt, grp, topk_idx, topk_w, ws, stream=None) -> None:
+    _take_router("moe_route4", cfg, x, w_gate, gate_bias)
+    _take_routing("moe_route4", cfg, topk_idx, topk_w)
     _check("moe_route4", lib().moe_route4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias),
                                           _opt(opt), _opt(grp), _p(topk_idx), _p(topk_w), _p(ws),
                                           ws.numel(), _s(stream)))

@@ -1,0 +1,55 @@
+"""What the bindings of the expert choice refuse before any launch (no GPU): outputs and
+inputs that the library would read or write past."""
+
+import pytest
+import torch
+
+from sparse_moe_transformer_gemm_b200 import build as moe_build
+from sparse_moe_transformer_gemm_b200 import moe
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+def refused(fn, *args, **kw):
+    with pytest.raises(moe.MoeError) as e:
+        fn(*args, stream=0, **kw)
+    assert e.value.code == moe.MOE_ERR_INVALID_ARG, e.value
+
+
+T, E, K, D, F = 4, 16, 2, 128, 128
+BAD_IDX = [torch.zeros(T, K, dtype=torch.int64), torch.zeros(T, 1, dtype=torch.int32),
+           torch.zeros(T, 2 * K, dtype=torch.int32)[:, ::2],
+           torch.zeros(K, T, dtype=torch.int32).t(), None]
+BAD_W = [torch.zeros(T, K, dtype=torch.bfloat16), torch.zeros(T - 1, K),
+         torch.zeros(T, K, dtype=torch.float64), torch.zeros(T, 2 * K)[:, ::2], None]
+
+
+def test_select_refuses_outputs_of_another_type_or_size():
+    cfg = moe.config(T, D, E, K, F)
+    z, idx, w = torch.zeros(T, E), torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+    for bad in BAD_IDX:
+        refused(moe.moe_select, cfg, z, None, None, bad, w)
+    for bad in BAD_W:
+        refused(moe.moe_select, cfg, z, None, None, idx, bad)
+
+
+def test_route4_refuses_outputs_of_another_type_or_size():
+    cfg = moe.config(T, D, E, K, F)
+    x, wg = torch.zeros(T, D, dtype=torch.bfloat16), torch.zeros(E, D, dtype=torch.bfloat16)
+    idx, w = torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+    ws = torch.zeros(moe.moe_workspace_size(cfg) + 256, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    for bad in BAD_IDX:
+        refused(moe.moe_route4, cfg, x, wg, None, None, None, bad, w, ws)
+    for bad in BAD_W:
+        refused(moe.moe_route4, cfg, x, wg, None, None, None, idx, bad, ws)
+    for bad in (x.float(), x[:3], torch.zeros(T, 2 * D, dtype=torch.bfloat16)[:, ::2]):
+        refused(moe.moe_route4, cfg, bad, wg, None, None, None, idx, w, ws)
+    for bad in (wg.float(), wg[:15]):
+        refused(moe.moe_route4, cfg, x, bad, None, None, None, idx, w, ws)
+    for bad in (torch.zeros(E - 1), torch.zeros(E, dtype=torch.bfloat16)):
+        refused(moe.moe_route4, cfg, x, wg, bad, None, None, idx, w, ws)
