@@ -380,6 +380,24 @@ def _take_router(fn: str, cfg, x, w_gate, gate_bias) -> None:
         _take(fn, gate_bias, torch.float32, cfg.E)
 
 
+def _take_bytes(fn: str, t: Optional[torch.Tensor], n: int) -> None:
+    """Refuse a tensor that is not n (or more) contiguous one-byte elements."""
+    if t is None or t.element_size() != 1 or t.numel() < n or not t.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+
+
+def _grouped(cfg):
+    """(experts, rows) of the grouped products, the shared expert's among them."""
+    shared = 1 if cfg.flags & MOE_FLAG_SHARED_EXPERT else 0
+    return cfg.E + shared, cfg.T * (cfg.k + shared)
+
+
+def _take_block(fn: str, codes, scales, rows: int, cols: int) -> None:
+    """Rows quantised in blocks of 128 columns."""
+    _take_bytes(fn, codes, rows * cols)
+    _take(fn, scales, torch.float32, rows * (cols // 128))
+
+
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
     if logits.dtype != torch.float32:
@@ -460,21 +478,35 @@ def moe_block_gemm(xq, sx, wq, sw, out, ws, offsets=None, stream=None) -> None:
 
 
 def moe_block_permute(cfg, x, row_of, xq, sx, stream=None) -> None:
-    _check("moe_block_permute", lib().moe_block_permute(ctypes.byref(cfg), _p(x), _p(row_of),
-                                                        _p(xq), _p(sx), _s(stream)))
+    fn, (_, R) = "moe_block_permute", _grouped(cfg)
+    _take(fn, x, torch.bfloat16, cfg.T * cfg.d)
+    _take(fn, row_of, torch.int32, R)
+    _take_block(fn, xq, sx, R, cfg.d)
+    _check(fn, lib().moe_block_permute(ctypes.byref(cfg), _p(x), _p(row_of), _p(xq), _p(sx),
+                                       _s(stream)))
 
 
 def moe_block_gate_up(cfg, xq, sx, offsets, w_gate_up, s_gate_up, hq, sh, ws, stream=None) -> None:
-    _check("moe_block_gate_up",
-           lib().moe_block_gate_up(ctypes.byref(cfg), _p(xq), _p(sx), _p(offsets), _p(w_gate_up),
-                                   _p(s_gate_up), _p(hq), _p(sh), _p(ws), ws.numel(),
-                                   _s(stream)))
+    fn, (E, R) = "moe_block_gate_up", _grouped(cfg)
+    _take_block(fn, xq, sx, R, cfg.d)
+    _take(fn, offsets, torch.int32, E + 1)
+    _take_bytes(fn, w_gate_up, E * 2 * cfg.d_ff * cfg.d)
+    _take(fn, s_gate_up, torch.float32, E * 2 * (cfg.d_ff // 128) * (cfg.d // 128))
+    _take_block(fn, hq, sh, R, cfg.d_ff)
+    _check(fn, lib().moe_block_gate_up(ctypes.byref(cfg), _p(xq), _p(sx), _p(offsets),
+                                       _p(w_gate_up), _p(s_gate_up), _p(hq), _p(sh), _p(ws),
+                                       ws.numel(), _s(stream)))
 
 
 def moe_block_down(cfg, hq, sh, offsets, w_down, s_down, y, ws, stream=None) -> None:
-    _check("moe_block_down",
-           lib().moe_block_down(ctypes.byref(cfg), _p(hq), _p(sh), _p(offsets), _p(w_down),
-                                _p(s_down), _p(y), _p(ws), ws.numel(), _s(stream)))
+    fn, (E, R) = "moe_block_down", _grouped(cfg)
+    _take_block(fn, hq, sh, R, cfg.d_ff)
+    _take(fn, offsets, torch.int32, E + 1)
+    _take_bytes(fn, w_down, E * cfg.d * cfg.d_ff)
+    _take(fn, s_down, torch.float32, E * (cfg.d // 128) * (cfg.d_ff // 128))
+    _take(fn, y, torch.bfloat16, R * cfg.d)
+    _check(fn, lib().moe_block_down(ctypes.byref(cfg), _p(hq), _p(sh), _p(offsets), _p(w_down),
+                                    _p(s_down), _p(y), _p(ws), ws.numel(), _s(stream)))
 
 
 def moe_read_status(ws, stream=None) -> int:

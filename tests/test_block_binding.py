@@ -53,3 +53,42 @@ def test_route4_refuses_outputs_of_another_type_or_size():
         refused(moe.moe_route4, cfg, x, bad, None, None, None, idx, w, ws)
     for bad in (torch.zeros(E - 1), torch.zeros(E, dtype=torch.bfloat16)):
         refused(moe.moe_route4, cfg, x, wg, bad, None, None, idx, w, ws)
+
+
+def worse(t):
+    """Tensors in t's place that must be refused: of a wider type, too few, strided, none."""
+    other = {torch.uint8: torch.int16, torch.int32: torch.int64, torch.float32: torch.float64,
+             torch.bfloat16: torch.float32}[t.dtype]
+    flat = torch.zeros(2 * t.numel(), dtype=t.dtype)
+    return [torch.zeros(t.shape, dtype=other), flat[:t.numel() - 1], flat[::2], None]
+
+
+def each_refused(fn, args, at):
+    """Every argument of `at` replaced by tensors that do not fit."""
+    for i in at:
+        for bad in worse(args[i]):
+            refused(fn, *args[:i], bad, *args[i + 1:])
+
+
+def step_args(shared):
+    """Arguments of moe_block_permute, moe_block_gate_up and moe_block_down."""
+    cfg = moe.config(T, D, E, K, F, fp8_block=True, shared=shared)
+    n, R = E + shared, T * (K + shared)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    f32 = torch.zeros
+    ws = u8(moe.moe_workspace_size(cfg) + 256)
+    ws = ws[-ws.data_ptr() % 256:]
+    xq, sx, hq, sh, off = u8(R, D), f32(R, D // 128), u8(R, F), f32(R, F // 128), i32(n + 1)
+    return (cfg, ws, [cfg, bf(T, D), i32(R), xq, sx],
+            [cfg, xq, sx, off, u8(n, 2 * F, D), f32(n, 2 * F // 128, D // 128), hq, sh, ws],
+            [cfg, hq, sh, off, u8(n, D, F), f32(n, D // 128, F // 128), bf(R, D), ws])
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_block_steps_refuse_tensors_that_do_not_fit(shared):
+    cfg, ws, permute, gate_up, down = step_args(shared)
+    each_refused(moe.moe_block_permute, permute, range(1, 5))
+    each_refused(moe.moe_block_gate_up, gate_up, range(1, 8))
+    each_refused(moe.moe_block_down, down, range(1, 7))
