@@ -398,6 +398,30 @@ def _take_block(fn: str, codes, scales, rows: int, cols: int) -> None:
     _take(fn, scales, torch.float32, rows * (cols // 128))
 
 
+def _take_weight(fn: str, cfg, w, s, rows: int, cols: int) -> None:
+    """One expert weight [experts, rows, cols] in cfg's format, with its scales."""
+    E = _grouped(cfg)[0]
+    if cfg.flags & MOE_FLAG_FP8_BLOCK:
+        _take_bytes(fn, w, E * rows * cols)
+        _take(fn, s, torch.float32, E * (rows // 128) * (cols // 128))
+    elif cfg.flags & MOE_FLAG_FP8_WEIGHTS:
+        _take_bytes(fn, w, E * rows * cols)
+        _take(fn, s, torch.float32, E * rows)
+    elif cfg.flags & MOE_FLAG_FP4_WEIGHTS:
+        _take_bytes(fn, w, E * rows * (cols // 2))
+        _take_bytes(fn, s, E * rows * (cols // 32))
+    else:
+        _take(fn, w, torch.bfloat16, E * rows * cols)
+        if s is not None:
+            raise MoeError(fn, MOE_ERR_INVALID_ARG)
+
+
+def _take_experts(fn: str, cfg, w_gate_up, s_gate_up, w_down, s_down, out) -> None:
+    _take_weight(fn, cfg, w_gate_up, s_gate_up, 2 * cfg.d_ff, cfg.d)
+    _take_weight(fn, cfg, w_down, s_down, cfg.d, cfg.d_ff)
+    _take(fn, out, torch.bfloat16, cfg.T * cfg.d)
+
+
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
     if logits.dtype != torch.float32:
@@ -418,6 +442,8 @@ def moe_route4(cfg, x, w_gate, gate_bias, opt, grp, topk_idx, topk_w, ws, stream
 
 def moe_forward4(cfg, x, w_gate, gate_bias, opt, grp, w_gate_up, s_gate_up, w_down, s_down, out,
                  ws, stream=None) -> None:
+    _take_router("moe_forward4", cfg, x, w_gate, gate_bias)
+    _take_experts("moe_forward4", cfg, w_gate_up, s_gate_up, w_down, s_down, out)
     _check("moe_forward4",
            lib().moe_forward4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias), _opt(opt),
                               _opt(grp), _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
@@ -427,6 +453,9 @@ def moe_forward4(cfg, x, w_gate, gate_bias, opt, grp, w_gate_up, s_gate_up, w_do
 def moe_forward_routed(cfg, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, out, ws,
                        stream=None) -> None:
     """The layer after its router, for a given routing."""
+    _take("moe_forward_routed", x, torch.bfloat16, cfg.T * cfg.d)
+    _take_routing("moe_forward_routed", cfg, topk_idx, topk_w)
+    _take_experts("moe_forward_routed", cfg, w_gate_up, s_gate_up, w_down, s_down, out)
     _check("moe_forward_routed",
            lib().moe_forward_routed(ctypes.byref(cfg), _p(x), _p(topk_idx), _p(topk_w),
                                     _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
@@ -490,8 +519,7 @@ def moe_block_gate_up(cfg, xq, sx, offsets, w_gate_up, s_gate_up, hq, sh, ws, st
     fn, (E, R) = "moe_block_gate_up", _grouped(cfg)
     _take_block(fn, xq, sx, R, cfg.d)
     _take(fn, offsets, torch.int32, E + 1)
-    _take_bytes(fn, w_gate_up, E * 2 * cfg.d_ff * cfg.d)
-    _take(fn, s_gate_up, torch.float32, E * 2 * (cfg.d_ff // 128) * (cfg.d // 128))
+    _take_weight(fn, cfg, w_gate_up, s_gate_up, 2 * cfg.d_ff, cfg.d)
     _take_block(fn, hq, sh, R, cfg.d_ff)
     _check(fn, lib().moe_block_gate_up(ctypes.byref(cfg), _p(xq), _p(sx), _p(offsets),
                                        _p(w_gate_up), _p(s_gate_up), _p(hq), _p(sh), _p(ws),
@@ -502,8 +530,7 @@ def moe_block_down(cfg, hq, sh, offsets, w_down, s_down, y, ws, stream=None) -> 
     fn, (E, R) = "moe_block_down", _grouped(cfg)
     _take_block(fn, hq, sh, R, cfg.d_ff)
     _take(fn, offsets, torch.int32, E + 1)
-    _take_bytes(fn, w_down, E * cfg.d * cfg.d_ff)
-    _take(fn, s_down, torch.float32, E * (cfg.d // 128) * (cfg.d_ff // 128))
+    _take_weight(fn, cfg, w_down, s_down, cfg.d, cfg.d_ff)
     _take(fn, y, torch.bfloat16, R * cfg.d)
     _check(fn, lib().moe_block_down(ctypes.byref(cfg), _p(hq), _p(sh), _p(offsets), _p(w_down),
                                     _p(s_down), _p(y), _p(ws), ws.numel(), _s(stream)))

@@ -92,3 +92,45 @@ def test_block_steps_refuse_tensors_that_do_not_fit(shared):
     each_refused(moe.moe_block_permute, permute, range(1, 5))
     each_refused(moe.moe_block_gate_up, gate_up, range(1, 8))
     each_refused(moe.moe_block_down, down, range(1, 7))
+
+
+# Expert weights a format takes: (config arguments, elements of an expert's weight rows of
+# n columns, their type, elements and type of the scales of r rows)
+FORMATS = {
+    "bf16": ({}, lambda n: n, torch.bfloat16, None),
+    "packed": (dict(packed=True), lambda n: n, torch.bfloat16, None),
+    "fp8": (dict(fp8=True), lambda n: n, torch.uint8, (lambda r, n: (r,), torch.float32)),
+    "fp4": (dict(fp4=True), lambda n: n // 2, torch.uint8,
+            (lambda r, n: (r, n // 32), torch.uint8)),
+    "fp8_block": (dict(fp8_block=True), lambda n: n, torch.uint8,
+                  (lambda r, n: (r // 128, n // 128), torch.float32)),
+    "bf16 shared": (dict(shared=True), lambda n: n, torch.bfloat16, None),
+    "fp8_block shared": (dict(shared=True, fp8_block=True), lambda n: n, torch.uint8,
+                         (lambda r, n: (r // 128, n // 128), torch.float32)),
+}
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_layers_refuse_tensors_that_do_not_fit(fmt):
+    kw, cols, wtype, scales = FORMATS[fmt]
+    d, f = 256, 512
+    cfg = moe.config(T, d, E, K, f, **kw)
+    n = E + int("shared" in fmt)
+    ws = torch.zeros(moe.moe_workspace_size(cfg) + 256, dtype=torch.uint8)
+    ws = ws[-ws.data_ptr() % 256:]
+    weights = []
+    for rows, width in ((2 * f, d), (d, f)):
+        weights.append(torch.zeros(n, rows, cols(width), dtype=wtype))
+        weights.append(None if scales is None
+                       else torch.zeros(n, *scales[0](rows, width), dtype=scales[1]))
+    x = torch.zeros(T, d, dtype=torch.bfloat16)
+    out = torch.zeros(T, d, dtype=torch.bfloat16)
+    idx, w = torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+    given = [i for i in range(4) if weights[i] is not None]
+    routed = [cfg, x, idx, w, *weights, out, ws]
+    each_refused(moe.moe_forward_routed, routed, [1, 2, 3, *(4 + i for i in given), 8])
+    wg = torch.zeros(E, d, dtype=torch.bfloat16)
+    whole = [cfg, x, wg, None, None, None, *weights, out, ws]
+    each_refused(moe.moe_forward4, whole, [1, 2, *(6 + i for i in given), 10])
+    if not scales:
+        refused(moe.moe_forward_routed, *routed[:5], torch.zeros(n, f), *routed[6:])
