@@ -362,15 +362,30 @@ def _rows(fn: str, t: torch.Tensor, rows: int, cols: int) -> int:
     return t.stride(0) if rows > 1 else max(cols, t.stride(0))
 
 
+def _on(fn: str, stream, first, *others):
+    """The stream's handle; refuses tensors that are not on the current device, on which
+    the call launches."""
+    device = first.get_device()  # -1: host memory
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    if device < 0 or device != torch.cuda.current_device():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _s(stream)
+
+
 def _take(fn: str, t: Optional[torch.Tensor], dtype: torch.dtype, n: int) -> None:
     """Refuse a tensor that is not n (or more) contiguous elements of dtype."""
-    if t is None or t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise MoeError(fn, MOE_ERR_INVALID_ARG)
 
 
 def _take_routing(fn: str, cfg, topk_idx, topk_w) -> None:
-    _take(fn, topk_idx, torch.int32, cfg.T * cfg.k)
-    _take(fn, topk_w, torch.float32, cfg.T * cfg.k)
+    n = cfg.T * cfg.k
+    _take(fn, topk_idx, torch.int32, n)
+    _take(fn, topk_w, torch.float32, n)
 
 
 def _take_router(fn: str, cfg, x, w_gate, gate_bias) -> None:
@@ -387,9 +402,9 @@ def _take_bytes(fn: str, t: Optional[torch.Tensor], n: int) -> None:
 
 
 def _grouped(cfg):
-    """(experts, rows) of the grouped products, the shared expert's among them."""
+    """(experts, rows, d, d_ff) of the grouped products, the shared expert's among them."""
     shared = 1 if cfg.flags & MOE_FLAG_SHARED_EXPERT else 0
-    return cfg.E + shared, cfg.T * (cfg.k + shared)
+    return cfg.E + shared, cfg.T * (cfg.k + shared), cfg.d, cfg.d_ff
 
 
 def _take_block(fn: str, codes, scales, rows: int, cols: int) -> None:
@@ -398,28 +413,28 @@ def _take_block(fn: str, codes, scales, rows: int, cols: int) -> None:
     _take(fn, scales, torch.float32, rows * (cols // 128))
 
 
-def _take_weight(fn: str, cfg, w, s, rows: int, cols: int) -> None:
-    """One expert weight [experts, rows, cols] in cfg's format, with its scales."""
-    E = _grouped(cfg)[0]
-    if cfg.flags & MOE_FLAG_FP8_BLOCK:
-        _take_bytes(fn, w, E * rows * cols)
-        _take(fn, s, torch.float32, E * (rows // 128) * (cols // 128))
-    elif cfg.flags & MOE_FLAG_FP8_WEIGHTS:
-        _take_bytes(fn, w, E * rows * cols)
-        _take(fn, s, torch.float32, E * rows)
-    elif cfg.flags & MOE_FLAG_FP4_WEIGHTS:
-        _take_bytes(fn, w, E * rows * (cols // 2))
-        _take_bytes(fn, s, E * rows * (cols // 32))
+def _take_weight(fn: str, flags: int, w, s, rows: int, cols: int) -> None:
+    """One expert weight, rows in all, in the format of flags, with its scales."""
+    if flags & MOE_FLAG_FP8_BLOCK:
+        _take_bytes(fn, w, rows * cols)
+        _take(fn, s, torch.float32, (rows // 128) * (cols // 128))
+    elif flags & MOE_FLAG_FP8_WEIGHTS:
+        _take_bytes(fn, w, rows * cols)
+        _take(fn, s, torch.float32, rows)
+    elif flags & MOE_FLAG_FP4_WEIGHTS:
+        _take_bytes(fn, w, rows * (cols // 2))
+        _take_bytes(fn, s, rows * (cols // 32))
     else:
-        _take(fn, w, torch.bfloat16, E * rows * cols)
+        _take(fn, w, torch.bfloat16, rows * cols)
         if s is not None:
             raise MoeError(fn, MOE_ERR_INVALID_ARG)
 
 
 def _take_experts(fn: str, cfg, w_gate_up, s_gate_up, w_down, s_down, out) -> None:
-    _take_weight(fn, cfg, w_gate_up, s_gate_up, 2 * cfg.d_ff, cfg.d)
-    _take_weight(fn, cfg, w_down, s_down, cfg.d, cfg.d_ff)
-    _take(fn, out, torch.bfloat16, cfg.T * cfg.d)
+    (E, _, d, F), flags = _grouped(cfg), cfg.flags
+    _take_weight(fn, flags, w_gate_up, s_gate_up, E * 2 * F, d)
+    _take_weight(fn, flags, w_down, s_down, E * d, F)
+    _take(fn, out, torch.bfloat16, cfg.T * d)
 
 
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
@@ -427,27 +442,31 @@ def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     if logits.dtype != torch.float32:
         raise MoeError("moe_select", MOE_ERR_INVALID_ARG)
     _take_routing("moe_select", cfg, topk_idx, topk_w)
+    st = _on("moe_select", stream, logits, topk_idx, topk_w)
     _check("moe_select", lib().moe_select(ctypes.byref(cfg), _p(logits),
                                           _rows("moe_select", logits, cfg.T, cfg.E), _opt(opt),
-                                          _opt(grp), _p(topk_idx), _p(topk_w), _s(stream)))
+                                          _opt(grp), _p(topk_idx), _p(topk_w), st))
 
 
 def moe_route4(cfg, x, w_gate, gate_bias, opt, grp, topk_idx, topk_w, ws, stream=None) -> None:
     _take_router("moe_route4", cfg, x, w_gate, gate_bias)
     _take_routing("moe_route4", cfg, topk_idx, topk_w)
+    st = _on("moe_route4", stream, x, w_gate, gate_bias, topk_idx, topk_w, ws)
     _check("moe_route4", lib().moe_route4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias),
                                           _opt(opt), _opt(grp), _p(topk_idx), _p(topk_w), _p(ws),
-                                          ws.numel(), _s(stream)))
+                                          ws.numel(), st))
 
 
 def moe_forward4(cfg, x, w_gate, gate_bias, opt, grp, w_gate_up, s_gate_up, w_down, s_down, out,
                  ws, stream=None) -> None:
     _take_router("moe_forward4", cfg, x, w_gate, gate_bias)
     _take_experts("moe_forward4", cfg, w_gate_up, s_gate_up, w_down, s_down, out)
+    st = _on("moe_forward4", stream, x, w_gate, gate_bias, w_gate_up, s_gate_up, w_down, s_down,
+             out, ws)
     _check("moe_forward4",
            lib().moe_forward4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias), _opt(opt),
                               _opt(grp), _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
-                              _p(out), _p(ws), ws.numel(), _s(stream)))
+                              _p(out), _p(ws), ws.numel(), st))
 
 
 def moe_forward_routed(cfg, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, out, ws,
@@ -456,10 +475,12 @@ def moe_forward_routed(cfg, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s
     _take("moe_forward_routed", x, torch.bfloat16, cfg.T * cfg.d)
     _take_routing("moe_forward_routed", cfg, topk_idx, topk_w)
     _take_experts("moe_forward_routed", cfg, w_gate_up, s_gate_up, w_down, s_down, out)
+    st = _on("moe_forward_routed", stream, x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down,
+             s_down, out, ws)
     _check("moe_forward_routed",
            lib().moe_forward_routed(ctypes.byref(cfg), _p(x), _p(topk_idx), _p(topk_w),
                                     _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),
-                                    _p(out), _p(ws), ws.numel(), _s(stream)))
+                                    _p(out), _p(ws), ws.numel(), st))
 
 
 def moe_block_quant(x, codes, scales, stream=None) -> None:
@@ -470,9 +491,10 @@ def moe_block_quant(x, codes, scales, stream=None) -> None:
             scales.dtype != torch.float32 or codes.element_size() != 1 or \
             not codes.is_contiguous() or not scales.is_contiguous():
         raise MoeError("moe_block_quant", MOE_ERR_INVALID_ARG)
+    st = _on("moe_block_quant", stream, x, codes, scales)
     _check("moe_block_quant",
            lib().moe_block_quant(_p(x), _rows("moe_block_quant", x, M, K), M, K, _p(codes),
-                                 _p(scales), _s(stream)))
+                                 _p(scales), st))
 
 
 def block_workspace(M: int, N: int, K: int, G: int = 1, device="cuda") -> torch.Tensor:
@@ -500,40 +522,43 @@ def moe_block_gemm(xq, sx, wq, sw, out, ws, offsets=None, stream=None) -> None:
             xq.element_size() != 1 or wq.element_size() != 1 or sx.dtype != torch.float32 or \
             sw.dtype != torch.float32 or not all(t.is_contiguous() for t in (xq, sx, wq, sw, out)):
         raise MoeError("moe_block_gemm", MOE_ERR_INVALID_ARG)
+    st = _on("moe_block_gemm", stream, xq, sx, wq, sw, out, ws, offsets)
     _check("moe_block_gemm",
            lib().moe_block_gemm(_p(xq), _p(sx), _p(wq), _p(sw), _p(offsets), G, M, N, K, _p(out),
                                 MOE_OUT_F32 if out.dtype == torch.float32 else MOE_OUT_BF16,
-                                _p(ws), ws.numel(), _s(stream)))
+                                _p(ws), ws.numel(), st))
 
 
 def moe_block_permute(cfg, x, row_of, xq, sx, stream=None) -> None:
-    fn, (_, R) = "moe_block_permute", _grouped(cfg)
-    _take(fn, x, torch.bfloat16, cfg.T * cfg.d)
+    fn, (_, R, d, _) = "moe_block_permute", _grouped(cfg)
+    _take(fn, x, torch.bfloat16, cfg.T * d)
     _take(fn, row_of, torch.int32, R)
-    _take_block(fn, xq, sx, R, cfg.d)
-    _check(fn, lib().moe_block_permute(ctypes.byref(cfg), _p(x), _p(row_of), _p(xq), _p(sx),
-                                       _s(stream)))
+    _take_block(fn, xq, sx, R, d)
+    st = _on(fn, stream, x, row_of, xq, sx)
+    _check(fn, lib().moe_block_permute(ctypes.byref(cfg), _p(x), _p(row_of), _p(xq), _p(sx), st))
 
 
 def moe_block_gate_up(cfg, xq, sx, offsets, w_gate_up, s_gate_up, hq, sh, ws, stream=None) -> None:
-    fn, (E, R) = "moe_block_gate_up", _grouped(cfg)
-    _take_block(fn, xq, sx, R, cfg.d)
+    fn, (E, R, d, F) = "moe_block_gate_up", _grouped(cfg)
+    _take_block(fn, xq, sx, R, d)
     _take(fn, offsets, torch.int32, E + 1)
-    _take_weight(fn, cfg, w_gate_up, s_gate_up, 2 * cfg.d_ff, cfg.d)
-    _take_block(fn, hq, sh, R, cfg.d_ff)
+    _take_weight(fn, MOE_FLAG_FP8_BLOCK, w_gate_up, s_gate_up, E * 2 * F, d)
+    _take_block(fn, hq, sh, R, F)
+    st = _on(fn, stream, xq, sx, offsets, w_gate_up, s_gate_up, hq, sh, ws)
     _check(fn, lib().moe_block_gate_up(ctypes.byref(cfg), _p(xq), _p(sx), _p(offsets),
                                        _p(w_gate_up), _p(s_gate_up), _p(hq), _p(sh), _p(ws),
-                                       ws.numel(), _s(stream)))
+                                       ws.numel(), st))
 
 
 def moe_block_down(cfg, hq, sh, offsets, w_down, s_down, y, ws, stream=None) -> None:
-    fn, (E, R) = "moe_block_down", _grouped(cfg)
-    _take_block(fn, hq, sh, R, cfg.d_ff)
+    fn, (E, R, d, F) = "moe_block_down", _grouped(cfg)
+    _take_block(fn, hq, sh, R, F)
     _take(fn, offsets, torch.int32, E + 1)
-    _take_weight(fn, cfg, w_down, s_down, cfg.d, cfg.d_ff)
-    _take(fn, y, torch.bfloat16, R * cfg.d)
+    _take_weight(fn, MOE_FLAG_FP8_BLOCK, w_down, s_down, E * d, F)
+    _take(fn, y, torch.bfloat16, R * d)
+    st = _on(fn, stream, hq, sh, offsets, w_down, s_down, y, ws)
     _check(fn, lib().moe_block_down(ctypes.byref(cfg), _p(hq), _p(sh), _p(offsets), _p(w_down),
-                                    _p(s_down), _p(y), _p(ws), ws.numel(), _s(stream)))
+                                    _p(s_down), _p(y), _p(ws), ws.numel(), st))
 
 
 def moe_read_status(ws, stream=None) -> int:

@@ -134,3 +134,57 @@ def test_layers_refuse_tensors_that_do_not_fit(fmt):
     each_refused(moe.moe_forward4, whole, [1, 2, *(6 + i for i in given), 10])
     if not scales:
         refused(moe.moe_forward_routed, *routed[:5], torch.zeros(n, f), *routed[6:])
+
+
+class Elsewhere:
+    """A tensor's attributes, on a device of its own."""
+
+    def __init__(self, t, index):
+        self.t, self.index = t, index
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        raise AssertionError("the call went on")
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("index", [-1, 1])
+def test_tensors_of_another_device_are_refused(monkeypatch, index):
+    """One tensor in host memory (-1), or on another device than the current one, which
+    would launch on it."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    cfg, ws, permute, gate_up, down = step_args(False)
+    plain = moe.config(T, D, E, K, F)
+    ws1 = torch.zeros(moe.moe_workspace_size(plain), dtype=torch.uint8)
+    x, out = torch.zeros(T, D, dtype=torch.bfloat16), torch.zeros(T, D, dtype=torch.bfloat16)
+    idx, w = torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+    wg, wgu = torch.zeros(E, D, dtype=torch.bfloat16), torch.zeros(E, 2 * F, D, dtype=torch.bfloat16)
+    wd, gb = torch.zeros(E, D, F, dtype=torch.bfloat16), torch.zeros(E)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    calls = [
+        (moe.moe_block_permute, permute, range(1, 5)),
+        (moe.moe_block_gate_up, gate_up, range(1, 9)),
+        (moe.moe_block_down, down, range(1, 8)),
+        (moe.moe_select, [plain, torch.zeros(T, E), None, None, idx, w], (1, 4, 5)),
+        (moe.moe_route4, [plain, x, wg, gb, None, None, idx, w, ws1], (1, 2, 3, 6, 7, 8)),
+        (moe.moe_forward_routed, [plain, x, idx, w, wgu, None, wd, None, out, ws1],
+         (1, 2, 3, 4, 6, 8, 9)),
+        (moe.moe_forward4, [plain, x, wg, gb, None, None, wgu, None, wd, None, out, ws1],
+         (1, 2, 3, 6, 8, 10, 11)),
+        (moe.moe_block_quant, [torch.zeros(4, 256, dtype=torch.bfloat16), u8(4, 256),
+                               torch.zeros(4, 2)], range(3)),
+        (moe.moe_block_gemm, [u8(4, 256), torch.zeros(4, 2), u8(2, 128, 256),
+                              torch.zeros(2, 1, 2), torch.zeros(4, 128), u8(256),
+                              torch.zeros(3, dtype=torch.int32)], range(7)),
+    ]
+    for fn, args, at in calls:
+        here = [Elsewhere(a, 0) if isinstance(a, torch.Tensor) else a for a in args]
+        # all on the current device: past the checks, to the pointers
+        with pytest.raises(AssertionError, match="went on"):
+            fn(*here, stream=0)
+        for i in at:
+            refused(fn, *here[:i], Elsewhere(args[i], index), *here[i + 1:])
