@@ -83,11 +83,17 @@ class MoeRouteOptions(ctypes.Structure):
 def route_options(score_bias=None, norm_weight=None, norm_eps: float = 1e-6,
                   score_fn: str = "sigmoid"):
     """Router options; score_fn is "sigmoid", "sqrtsoftplus" or, for moe_select, moe_route4
-    and moe_forward4, "softmax" (or a MOE_SCORE_* value)."""
+    and moe_forward4, "softmax" (or a MOE_SCORE_* value). The tensors, contiguous fp32, live
+    as long as the options."""
     fn = SCORE_FNS[score_fn] if isinstance(score_fn, str) else int(score_fn)
-    return MoeRouteOptions(None if score_bias is None else score_bias.data_ptr(),
-                           None if norm_weight is None else norm_weight.data_ptr(),
-                           float(norm_eps), fn)
+    for t in (score_bias, norm_weight):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+            raise MoeError("route_options", MOE_ERR_INVALID_ARG)
+    opt = MoeRouteOptions(None if score_bias is None else score_bias.data_ptr(),
+                          None if norm_weight is None else norm_weight.data_ptr(),
+                          float(norm_eps), fn)
+    opt.tensors = (score_bias, norm_weight)
+    return opt
 
 
 class MoeGroupOptions(ctypes.Structure):

@@ -188,3 +188,27 @@ def test_tensors_of_another_device_are_refused(monkeypatch, index):
             fn(*here, stream=0)
         for i in at:
             refused(fn, *here[:i], Elsewhere(args[i], index), *here[i + 1:])
+
+
+def test_route_options_keep_their_tensors():
+    """The library reads them through pointers: a temporary lives as long as the options."""
+    gone = []
+
+    class Watched(torch.Tensor):
+        def __del__(self):
+            gone.append(1)
+
+    opt = moe.route_options(torch.ones(E).as_subclass(Watched),
+                            torch.ones(D).as_subclass(Watched))
+    assert not gone and opt.score_bias and opt.norm_weight
+    del opt
+    assert len(gone) == 2
+
+
+def test_route_options_refuse_other_types_and_layouts():
+    for bad in (torch.ones(E, dtype=torch.bfloat16), torch.ones(E, dtype=torch.float64),
+                torch.ones(2 * E)[::2]):
+        for kw in (dict(score_bias=bad), dict(norm_weight=bad)):
+            with pytest.raises(moe.MoeError) as e:
+                moe.route_options(**kw)
+            assert e.value.code == moe.MOE_ERR_INVALID_ARG
