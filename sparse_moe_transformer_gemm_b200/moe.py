@@ -394,6 +394,14 @@ def _take_routing(fn: str, cfg, topk_idx, topk_w) -> None:
     _take(fn, topk_w, torch.float32, n)
 
 
+def _options(fn: str, cfg, opt):
+    """(score_bias, norm_weight) of opt, as route_options made it."""
+    bias, norm = getattr(opt, "tensors", (None, None))
+    if (bias is not None and bias.numel() < cfg.E) or (norm is not None and norm.numel() < cfg.d):
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return bias, norm
+
+
 def _take_router(fn: str, cfg, x, w_gate, gate_bias) -> None:
     _take(fn, x, torch.bfloat16, cfg.T * cfg.d)
     _take(fn, w_gate, torch.bfloat16, cfg.E * cfg.d)
@@ -445,19 +453,26 @@ def _take_experts(fn: str, cfg, w_gate_up, s_gate_up, w_down, s_down, out) -> No
 
 def moe_select(cfg, logits, opt, grp, topk_idx, topk_w, stream=None) -> None:
     """The choice of experts from logits [T, E] fp32 (rows may be strided)."""
-    if logits.dtype != torch.float32:
-        raise MoeError("moe_select", MOE_ERR_INVALID_ARG)
-    _take_routing("moe_select", cfg, topk_idx, topk_w)
-    st = _on("moe_select", stream, logits, topk_idx, topk_w)
-    _check("moe_select", lib().moe_select(ctypes.byref(cfg), _p(logits),
-                                          _rows("moe_select", logits, cfg.T, cfg.E), _opt(opt),
-                                          _opt(grp), _p(topk_idx), _p(topk_w), st))
+    fn, T, E = "moe_select", cfg.T, cfg.E
+    if logits.dtype is not torch.float32:
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    ld = _rows(fn, logits, T, E)
+    _take_routing(fn, cfg, topk_idx, topk_w)
+    if opt is None:
+        st = _on(fn, stream, logits, topk_idx, topk_w)
+    else:
+        st = _on(fn, stream, logits, topk_idx, topk_w, *_options(fn, cfg, opt))
+    rc = lib().moe_select(ctypes.byref(cfg), logits.data_ptr(), ld, _opt(opt), _opt(grp),
+                          topk_idx.data_ptr(), topk_w.data_ptr(), st)
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
 
 
 def moe_route4(cfg, x, w_gate, gate_bias, opt, grp, topk_idx, topk_w, ws, stream=None) -> None:
     _take_router("moe_route4", cfg, x, w_gate, gate_bias)
     _take_routing("moe_route4", cfg, topk_idx, topk_w)
-    st = _on("moe_route4", stream, x, w_gate, gate_bias, topk_idx, topk_w, ws)
+    st = _on("moe_route4", stream, x, w_gate, gate_bias, topk_idx, topk_w, ws,
+             *_options("moe_route4", cfg, opt))
     _check("moe_route4", lib().moe_route4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias),
                                           _opt(opt), _opt(grp), _p(topk_idx), _p(topk_w), _p(ws),
                                           ws.numel(), st))
@@ -468,7 +483,7 @@ def moe_forward4(cfg, x, w_gate, gate_bias, opt, grp, w_gate_up, s_gate_up, w_do
     _take_router("moe_forward4", cfg, x, w_gate, gate_bias)
     _take_experts("moe_forward4", cfg, w_gate_up, s_gate_up, w_down, s_down, out)
     st = _on("moe_forward4", stream, x, w_gate, gate_bias, w_gate_up, s_gate_up, w_down, s_down,
-             out, ws)
+             out, ws, *_options("moe_forward4", cfg, opt))
     _check("moe_forward4",
            lib().moe_forward4(ctypes.byref(cfg), _p(x), _p(w_gate), _p(gate_bias), _opt(opt),
                               _opt(grp), _p(w_gate_up), _p(s_gate_up), _p(w_down), _p(s_down),

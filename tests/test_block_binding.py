@@ -212,3 +212,25 @@ def test_route_options_refuse_other_types_and_layouts():
             with pytest.raises(moe.MoeError) as e:
                 moe.route_options(**kw)
             assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("index", [0, -1, 1])
+def test_options_that_do_not_fit_the_call(monkeypatch, index):
+    """A bias of fewer than E experts, a norm weight of fewer than d columns, and (index
+    other than 0) options whose tensors are on another device than the call's."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    at0 = lambda *s, t=torch.float32: Elsewhere(torch.zeros(*s, dtype=t), 0)  # noqa: E731
+    cfg = moe.config(T, D, E, K, F)
+    ws = Elsewhere(torch.zeros(moe.moe_workspace_size(cfg), dtype=torch.uint8), 0)
+    x, wg = at0(T, D, t=torch.bfloat16), at0(E, D, t=torch.bfloat16)
+    idx, w = at0(T, K, t=torch.int32), at0(T, K)
+    wgu, wd = at0(E, 2 * F, D, t=torch.bfloat16), at0(E, D, F, t=torch.bfloat16)
+    out = at0(T, D, t=torch.bfloat16)
+    short = 0 if index else 1
+    for kw in (dict(score_bias=torch.zeros(E - short)), dict(norm_weight=torch.zeros(D - short))):
+        opt = moe.route_options(**kw)
+        opt.tensors = [t if t is None else Elsewhere(t, index) for t in opt.tensors]
+        refused(moe.moe_route4, cfg, x, wg, None, opt, None, idx, w, ws)
+        refused(moe.moe_forward4, cfg, x, wg, None, opt, None, wgu, None, wd, None, out, ws)
+        if "score_bias" in kw:
+            refused(moe.moe_select, cfg, at0(T, E), opt, None, idx, w)
