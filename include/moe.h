@@ -311,10 +311,11 @@ MOE_API int moe_forward3(const moe_config* cfg, const void* x, const void* w_gat
 MOE_API int moe_ep_row_experts(const int32_t* counts, int32_t n_src, int32_t E_local,
                                int32_t* expert_of_row, int32_t n_rows, void* stream);
 
-/* Failure-detection self-test: one thread waits, with the library's bounded
- * wait and a limit of limit_ns (1 ns .. 10 s), on an mbarrier that nothing
- * completes, then records MOE_ERR_TIMEOUT in the status word of ws (read it
- * with moe_read_status). Faults, traps and hangs nothing; the context stays
+/* Failure-detection self-test: one thread waits, with each of the library's two
+ * bounded waits and a limit of limit_ns (1 ns .. 10 s), on an mbarrier that nothing
+ * completes, and once more with the abort flag raised, which ends the wait; then it
+ * records MOE_ERR_TIMEOUT in the status word of ws (read it with
+ * moe_read_status). Faults, traps and hangs nothing; the context stays
  * usable. Not part of the layer (the pages have no counterpart). */
 MOE_API int moe_selftest_bounded_wait(void* ws, unsigned long long limit_ns, void* stream);
 

@@ -6,8 +6,11 @@
 // records MOE_ERR_TIMEOUT in the workspace status word and returns, so the
 // host reads the error with moe_read_status and the CUDA context stays usable.
 // This entry point runs that path on purpose: one thread initialises an
-// mbarrier that nothing ever arrives on and waits on it with the same bounded
-// wait the kernels use (a caller-chosen limit).
+// mbarrier that nothing ever arrives on and waits on it with the bounded waits the
+// kernels use: the plain one and the pipelines' (mbar_wait_hot_at) with a
+// caller-chosen limit each, and the latter with the kernels' own limit and the abort
+// flag raised, which ends it at once. The status is MOE_ERR_TIMEOUT if all three
+// gave up.
 #include "internal.h"
 #include "tc.cuh"
 
@@ -20,8 +23,12 @@ __global__ void bounded_wait_kernel(unsigned long long limit_ns, int* status) {
         abort_flag = 0;
         moe::tc::mbar_init(&bar, 1);
         moe::tc::fence_mbar_init();
-        if (!moe::tc::mbar_wait_for(&bar, 0, &abort_flag, limit_ns))
-            atomicExch(status, MOE_ERR_TIMEOUT);
+        const uint32_t at = moe::tc::smem_u32(&bar);
+        const bool plain = moe::tc::mbar_wait_for(&bar, 0, &abort_flag, limit_ns);
+        const bool hot = moe::tc::mbar_wait_hot_at(at, 0, &abort_flag, limit_ns);
+        *reinterpret_cast<volatile int*>(&abort_flag) = 1;
+        const bool told = moe::tc::mbar_wait_hot_at(at, 0, &abort_flag);
+        if (!plain && !hot && !told) atomicExch(status, MOE_ERR_TIMEOUT);
     }
 }
 

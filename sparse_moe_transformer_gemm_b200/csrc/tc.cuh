@@ -109,14 +109,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
 // whose roles' loops do not fit the instruction cache together loses a factor of
 // two).
 __device__ __forceinline__ bool mbar_wait_hot_at(uint32_t addr, uint32_t parity,
-                                                 const volatile int* abort_flag) {
+                                                 const volatile int* abort_flag,
+                                                 uint64_t limit_ns = kWaitNs) {
     uint64_t t0 = 0;
 #pragma unroll 1
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait_at(addr, parity)) return true;
         if ((i & 1023u) == 0u) {
             const uint64_t now = globaltimer_ns();
-            if (*abort_flag || (t0 && now - t0 > kWaitNs)) return false;
+            if (*abort_flag || (t0 && now - t0 > limit_ns)) return false;
             if (!t0) t0 = now;
         }
     }
