@@ -53,7 +53,8 @@ constexpr int THREADS = 32 * (PROMO_WARP + 8);
 // Registers a thread with tiles of 128 tokens, whose promotion holds 128
 // accumulators: 168 at launch; 3 * 168 = 72 + 2 * 216.
 constexpr int REGS_FEW = 72, REGS_MANY = 216;
-static_assert(REGS_FEW + 2 * REGS_MANY == 3 * 168, "no more than the launch gave");
+constexpr tc::RegSplit REGS = {REGS_FEW, REGS_MANY, 2};
+static_assert(tc::split_fits(REGS, 168) && !tc::split_fits(REGS, 160), "all of a launch with 168");
 // Up to so many rows a group on average, tiles of 64 tokens.
 constexpr long kFewRows64 = 32;
 
@@ -525,7 +526,8 @@ template <bool GATE_UP, bool OUT_F32, int NM>
 cudaError_t launch(const CUtensorMap& ma, const TokenMaps& mb, const Args& a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     auto kernel = block_few_kernel<GATE_UP, OUT_F32, NM>;
-    const cudaError_t err = allow_smem((const void*)kernel, smem_bytes<NM>(), done);
+    const cudaError_t err = allow_smem((const void*)kernel, smem_bytes<NM>(), done,
+                                       NM == 128 ? REGS : tc::RegSplit{});
     return err != cudaSuccess
                ? err
                : launch_pairs(kernel, sm_pairs(), THREADS, smem_bytes<NM>(), s, ma, mb, a);

@@ -53,12 +53,17 @@ bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64
     return true;
 }
 
-cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done) {
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done,
+                       const tc::RegSplit& split) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaFuncAttributes attr;
+    err = cudaFuncGetAttributes(&attr, kernel);
+    if (err != cudaSuccess) return err;
+    if (!tc::split_fits(split, attr.numRegs)) return cudaErrorLaunchOutOfResources;
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return err;

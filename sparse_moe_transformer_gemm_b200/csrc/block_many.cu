@@ -64,7 +64,8 @@ constexpr int SLOTS = 2;
 constexpr int EPI_BYTES = 4 * GROUPS * 32 * 32;  // a [32 tokens][32 bytes] store tile per warp
 // registers a thread: 168 at launch; 3 * 168 = 72 + 2 * 216
 constexpr int REGS_FEW = 72, REGS_MANY = 216;
-static_assert(REGS_FEW + GROUPS * REGS_MANY == (1 + GROUPS) * 168, "no more than the launch gave");
+constexpr tc::RegSplit REGS = {REGS_FEW, REGS_MANY, GROUPS};
+static_assert(tc::split_fits(REGS, 168) && !tc::split_fits(REGS, 160), "all of a launch with 168");
 
 struct Ctrl {
     uint64_t full[STAGES];    // even CTA: TMA bytes of both CTAs landed
@@ -474,7 +475,7 @@ template <bool GATE_UP, bool OUT_F32>
 cudaError_t launch(const CUtensorMap& ma, const TokenMaps& mb, const Args& a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     auto kernel = block_many_kernel<GATE_UP, OUT_F32>;
-    const cudaError_t err = allow_smem((const void*)kernel, SMEM, done);
+    const cudaError_t err = allow_smem((const void*)kernel, SMEM, done, REGS);
     return err != cudaSuccess ? err : launch_pairs(kernel, sm_pairs(), THREADS, SMEM, s, ma, mb, a);
 }
 

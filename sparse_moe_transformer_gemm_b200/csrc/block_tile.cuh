@@ -1,4 +1,4 @@
-// block_tile.cuh -- what the two block-FP8 product kernels share: the arguments,
+// block_tile.cuh -- what the three block-FP8 product kernels share: the arguments,
 // the table of tiles and the tensor maps.
 #pragma once
 
@@ -163,7 +163,9 @@ bool make_token_byte_maps(TokenMaps* tm, const void* base, uint64_t rows, uint64
 int sm_pairs();
 
 // A kernel's shared-memory limit, set once per device (`done`: a bit per device).
-cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done);
+// cudaErrorLaunchOutOfResources: it was compiled to fewer registers than it hands over.
+cudaError_t allow_smem(const void* kernel, int smem, std::atomic<uint64_t>& done,
+                       const tc::RegSplit& split = {});
 
 // The kernel on `pairs` pairs of SMs (allow_smem comes first).
 template <typename Kernel>

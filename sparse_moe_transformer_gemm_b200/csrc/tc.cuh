@@ -304,7 +304,9 @@ __device__ __forceinline__ void cp_async_wait_pending() {
 }
 
 // Give up registers to, or take them from, the block's pool (all four warps of a
-// warpgroup; the shares have to add up to at most what the launch allocated).
+// warpgroup). The shares have to add up to at most what the launch allocated: a
+// warpgroup that asks for more waits for good, in a wait without a limit, so the host
+// looks at the compiled kernel before its first launch (split_fits).
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -312,6 +314,15 @@ __device__ __forceinline__ void regs_dec() {
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Registers a thread that one warpgroup keeps and `groups` others take (0: no split).
+struct RegSplit {
+    int few = 0, many = 0, groups = 0;
+};
+// Whether a launch with `regs` a thread (allocated in steps of 8) covers the split.
+__host__ __device__ constexpr bool split_fits(const RegSplit& s, int regs) {
+    return s.groups == 0 || s.few + s.groups * s.many <= (1 + s.groups) * ((regs + 7) / 8 * 8);
 }
 
 // ------------------------------------------------------------------ tcgen05
