@@ -366,20 +366,10 @@ cudaError_t launch(const BlockGemm& p, int S, cudaStream_t s) {
 
 }  // namespace
 
-// One product whose tiles of 128 rows (and up to 32 tokens, or 128) fit the SMs at
-// once: as many slices of K, at most 8 (the portable cluster size), as still run at
-// once; 0 for more tiles than SMs. Measured against the pair kernels: 128 x 4096 x 4096
-// (32 tiles) 10.2 us and 31, 512 x 2048 x 4096 (64) 13.7 and 23, 512 x 4096 x 4096 (128,
-// uncut) 21.3 and 23.8, 200 x 256 x 128 (4, one block) 6.8 and 6.8.
 int splits(const BlockGemm& p) {
     if (p.offsets) return 0;
     const long token_tiles = p.M <= 32 ? 1 : (p.M + 127) / 128;
-    const long tiles = (p.N + BM - 1) / BM * token_tiles, sms = 2L * sm_pairs();
-    if (tiles > sms) return 0;
-    const int KB = (p.K + BK - 1) / BK;
-    int S = 1;
-    while (S < 8 && 2 * S * tiles <= sms && 2 * S <= KB) S *= 2;
-    return S;
+    return slices_of((p.N + BM - 1) / BM * token_tiles, (p.K + BK - 1) / BK, 2 * sm_pairs());
 }
 
 cudaError_t launch_split(const BlockGemm& p, cudaStream_t s) {

@@ -189,8 +189,27 @@ cudaError_t launch_pairs(Kernel kernel, int pairs, int threads, int smem, cudaSt
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// The kernels' launchers (block_split.cu, block_few.cu, block_many.cu); splits: K slices
-// of block_split's kernel, 0 where it does not take the product.
+// K slices of one product whose tiles of 128 weight rows (and up to 32 tokens, or 128) fit
+// the SMs at once: the most, up to 8 (the portable cluster size) and the blocks of K,
+// with which all clusters run at once; 0 for more tiles than SMs. A cluster's SMs lie
+// in one GPC, and of its CTAs an SM holds one, so that a B200's 148 SMs take 15
+// clusters of 8 and 33 of 4 (cudaOccupancyMaxActiveClusters on four GPUs), not 18 and 37.
+// Constants, not the device's answer: a product has the same bits on every GPU.
+// Measured at K = 4096, M = 1, with 8 / 4 / 2 slices: 15 tiles 5.0 / 5.7 / 7.8 us, 16 tiles
+// 8.9 / 5.7 / 7.8, 33 tiles 13.6 / 6.1 / 7.9, 34 tiles 13.7 / 10.7 / 7.9, 74 tiles - / 16.4
+// / 8.2 (uncut 12.1); M = 128: 15 tiles 8.1 / 8.8 / 11.9, 16 tiles 14.4 / 8.7 / 11.9, 33
+// tiles 22.0 / 9.2 / 12.1, 34 tiles 22.2 / 16.5 / 12.1. Against the pair kernels: 128 x 4096
+// x 4096 (32 tiles) 10.2 us and 31, 512 x 2048 x 4096 (64) 13.7 and 23, 512 x 4096 x 4096
+// (128, uncut) 21.3 and 23.8, 200 x 256 x 128 (4, one block) 6.8 and 6.8.
+__host__ __device__ constexpr int slices_of(long tiles, int blocks, int sms) {
+    if (tiles > sms) return 0;
+    int S = tiles <= 15 ? 8 : tiles <= 33 ? 4 : 2;
+    while (S > 1 && (S * tiles > sms || S > blocks)) S /= 2;
+    return S;
+}
+
+// The kernels' launchers (block_split.cu, block_few.cu, block_many.cu); splits: slices_of
+// a product for block_split's kernel, 0 where it does not take it.
 int splits(const BlockGemm& p);
 cudaError_t launch_split(const BlockGemm& p, cudaStream_t s);
 cudaError_t launch_few(const BlockGemm& p, bool gate_up, cudaStream_t s);
