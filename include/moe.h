@@ -47,8 +47,10 @@
  *   the scale of each 128 x 128 block (16-byte aligned). The activations are
  *   quantised by the library as moe_block_quant says, x before gate_up and
  *   h = SiLU(g) * u (fp32) before down, and the products run on the FP8 tensor
- *   cores (moe_block_gemm's arithmetic). With any other weight format,
- *   MOE_FLAG_PACKED_WEIGHTS or MOE_FLAG_STREAM_PATH: MOE_ERR_INVALID_ARG.
+ *   cores (moe_block_gemm's arithmetic). An expert's output is rounded to bf16,
+ *   as in the other formats, before the weighted sum in fp32. With any other
+ *   weight format, MOE_FLAG_PACKED_WEIGHTS or MOE_FLAG_STREAM_PATH:
+ *   MOE_ERR_INVALID_ARG.
  *   moe_expert_gate_up, moe_expert_gate_up_gather and moe_expert_down, whose
  *   h is bf16, refuse it (MOE_ERR_INVALID_ARG): moe_block_gate_up and
  *   moe_block_down take their place.

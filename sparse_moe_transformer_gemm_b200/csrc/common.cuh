@@ -210,9 +210,6 @@ __device__ __forceinline__ void warp_select_topk(float (&sc)[8], int k, float sc
     }
 }
 
-// SwiGLU's SiLU(g) * u with the fast exponential and division intrinsics: their
-// relative error (~1e-6) sits far below the bf16 rounding of the result
-// (2^-9), and for g below about -87 the quotient is 0, SiLU's limit.
 // Programmatic dependent launch: let the next kernel on the stream begin
 // launching (its thread blocks take SMs as this grid's leave, and wait in
 // their own pdl_launch_and_wait), then wait until the previous kernel on the
@@ -228,6 +225,9 @@ __device__ __forceinline__ void pdl_launch() {
 }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// SwiGLU's SiLU(g) * u with the fast exponential and division intrinsics: their
+// relative error (~1e-6) sits far below the rounding of the result (half a step: 2^-8
+// in bf16, 2^-4 in e4m3), and for g below about -87 the quotient is 0, SiLU's limit.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fdividef(g, 1.0f + __expf(-g)) * u;
 }

@@ -20,11 +20,17 @@
 // tokens of five, which the order of the candidates settles: T = 16384 without a bias
 // 13.0 us and 20.1, the softmax 13.4 and 20.6 (28.4 where it repeated whole tokens).
 //
-// Bound: about 600 instructions per token against 4 E bytes read. Measured, E =
-// 256, top-8, T = 16384: 13.5 us without a bias or groups (reading the logits
-// takes 2.6); biased, E = 192 17.6 us; biased, 4 of 8 groups by their two best 25.8
-// us, of which 4 are the latency of tokens with an open group (30 before the
-// candidates had an order of their own). T = 64: 2.8 us, the launch's.
+// Groups that do not fit a warp at 8 experts a lane, whole lanes and a power of two of
+// them a group (E = 240 in 3, 5, 6 or 10 groups; more than 32 groups), take
+// select_exactly for every token: T = 16384, E = 240 biased in 10 groups 65 us, in 8 27.
+//
+// Bound: instructions, about 600 a token without groups and 1000 with them, against
+// 4 E bytes read. While its warps run, an SM issues in 70% of its cycles, its alu pipe
+// is 56 to 60% busy, and a warp waits mostly for fixed latencies and its turn; the
+// launch and the last tokens are the rest. Measured, E = 256, top-8, T = 16384, back
+// to back: 13.0 us without a bias or groups (reading the logits takes 2.6); biased, E =
+// 192 17.1 us; biased, 4 of 8 groups by their two best 25.6 us, of which 4 are the
+// latency of tokens with an open group. T = 64: 2.8 us, the launch's.
 #include <float.h>
 
 #include "common.cuh"
@@ -36,7 +42,7 @@ namespace {
 constexpr int WARPS = 4;      // tokens per CTA
 constexpr int Q = 8;          // experts per lane
 constexpr int PAD_E = 256 + 8;
-constexpr int kCtasPerSm = 7;  // persistent CTAs: 8 spill registers, 6 leave issue slots
+constexpr int kCtasPerSm = 7;  // persistent CTAs: 8 spill in the token loop, 6 leave issue slots
 
 struct SelectArgs {
     const float* logits;
@@ -314,8 +320,9 @@ __device__ __noinline__ int order_exactly(const SelectArgs& a, const float* row,
     return mine;
 }
 
-// Lane j < k: the weight of its expert from that expert's logit zj; z and zmax (the
-// softmax's reference) are the token's. Where the weights are divided by their
+// Lane j < k: the weight of its expert from that expert's logit zj, in fp32 (the
+// exponentials within 2 ulp, one division: 4e-6 of the weight at most, which scales a
+// bf16 output); z and zmax (the softmax's reference) are the token's. Where the weights are divided by their
 // sum, a common factor is free: the softmax takes the largest chosen logit as its
 // reference, and scores of logits so small that fp32 would lose them (sigmoid(z)
 // = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are taken relative to the
@@ -505,7 +512,8 @@ select_kernel(const __grid_constant__ SelectArgs a, int lanes) {
     }
 }
 
-// Groups that do not fit a warp's lanes (more than 32 / lanes of them).
+// Groups that do not fit a warp's lanes (more than 32 / lanes of them): every token in
+// fp64 where scores are compared, the measured cost of which the header gives.
 __global__ void __launch_bounds__(WARPS * 32, kCtasPerSm)
 select_exact_kernel(const __grid_constant__ SelectArgs a) {
     pdl_launch_and_wait();
