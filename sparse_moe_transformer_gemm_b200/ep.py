@@ -339,7 +339,12 @@ def local_expert_weights(part: Partition, rank: int, w_gate_up, w_down, s_gate_u
 
     def pick(t):
         t = None if t is None else t[sl]
-        return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+        if t is None or t.data_ptr() % 16 == 0:
+            return t
+        t = t.clone()
+        if t.is_cuda:  # the rank may run on another stream
+            torch.cuda.current_stream(t.device).synchronize()
+        return t
 
     return pick(w_gate_up), pick(s_gate_up), pick(w_down), pick(s_down)
 

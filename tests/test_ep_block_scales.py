@@ -48,3 +48,40 @@ def test_ranks_equal_the_layer_on_one_gpu(d, F, T, E, k, P):
         ws, want = moe.workspace(one), torch.empty_like(c)
         moe.moe_forward(one, c, wg, None, *weights, want, ws)
         assert torch.equal(out, want) and moe.moe_read_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.gpu
+def test_the_copied_scales_are_ready_on_any_stream():
+    """The rank is made behind long work on one stream and runs on another."""
+    moe_build.build()
+    T, E, k, d, F, P = 24, 4, 2, 128, 128, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    gu = [ref.random_weight(g, 2 * F, d) for _ in range(E)]
+    dn = [ref.random_weight(g, d, F) for _ in range(E)]
+    weights = [torch.stack([p[i] for p in ws]) for ws in (gu, dn) for i in (0, 1)]
+    x = torch.randn(T, d, generator=g, device="cuda").to(torch.bfloat16)
+    wg = (torch.randn(E, d, generator=g, device="cuda") * 0.05).to(torch.bfloat16)
+    cfg = moe.config(T, d, E, k, F, fp8_block=True)
+    part = ep.Partition(E, P)
+    xs = [c.contiguous() for c in torch.chunk(x, P)]
+
+    def outputs():
+        ops = [ep.ep_layer_ops(cfg, part, r, wg, None, *weights) for r in range(P)]
+        other = torch.cuda.Stream()
+        with torch.cuda.stream(other):
+            outs = ep.ep_forward_lockstep(ops, part, xs)
+        torch.cuda.synchronize()
+        return outs
+
+    first = outputs()
+    torch.cuda.synchronize()
+    a = torch.randn(8192, 8192, device="cuda")
+    for _ in range(3):
+        junk = [torch.full((64,), float("nan"), device="cuda") for _ in range(64)]
+        del junk
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a @ a  # some tens of milliseconds
+        for got, want in zip(outputs(), first):
+            assert torch.equal(got, want)
