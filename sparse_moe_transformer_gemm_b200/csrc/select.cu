@@ -322,11 +322,11 @@ __device__ __noinline__ int order_exactly(const SelectArgs& a, const float* row,
 
 // Lane j < k: the weight of its expert from that expert's logit zj, in fp32 (the
 // exponentials within 2 ulp, one division: 4e-6 of the weight at most, which scales a
-// bf16 output); z and zmax (the softmax's reference) are the token's. Where the weights are divided by their
-// sum, a common factor is free: the softmax takes the largest chosen logit as its
-// reference, and scores of logits so small that fp32 would lose them (sigmoid(z)
-// = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are taken relative to the
-// largest one's.
+// bf16 output); z and zmax (the softmax's reference) are the token's. Where the weights
+// are divided by their sum, a common factor is free: the softmax takes the largest
+// chosen logit as its reference, and scores of logits so small that fp32 would lose
+// them (sigmoid(z) = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are taken
+// relative to the largest one's.
 __device__ __forceinline__ float weight_of(const SelectArgs& a, int fn, const float (&z)[Q],
                                            float zmax, float zj) {
     float s;
