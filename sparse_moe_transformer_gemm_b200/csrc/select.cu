@@ -22,7 +22,7 @@
 //
 // Groups that do not fit a warp at 8 experts a lane, whole lanes and a power of two of
 // them a group (E = 240 in 3, 5, 6 or 10 groups; more than 32 groups), take
-// select_exactly for every token: T = 16384, E = 240 biased in 10 groups 65 us, in 8 27.
+// select_exactly for every token: T = 16384, E = 240 biased in 10 groups 66 us, in 8 27.
 //
 // Bound: instructions, about 600 a token without groups and 1000 with them, against
 // 4 E bytes read. While its warps run, an SM issues in 70% of its cycles, its alu pipe
@@ -103,7 +103,10 @@ __device__ __forceinline__ float score_of(float z, int fn) {
     return __fdividef(1.0f, 1.0f + __expf(-z));
 }
 __device__ __forceinline__ double score_of(double z, int fn) {
-    if (fn == MOE_SCORE_SQRT_SOFTPLUS) return sqrt(fmax(z, 0.0) + log1p(exp(-fabs(z))));
+    // the smallest scores, down to fp64's subnormals: e^z and e^(z/2) to 1e-17
+    const bool root = fn == MOE_SCORE_SQRT_SOFTPLUS;
+    if (z < -700.0) return exp(root ? 0.5 * z : z);
+    if (root) return sqrt(fmax(z, 0.0) + log1p(exp(-fabs(z))));
     return 1.0 / (1.0 + exp(-z));
 }
 
@@ -320,28 +323,37 @@ __device__ __noinline__ int order_exactly(const SelectArgs& a, const float* row,
     return mine;
 }
 
-// Lane j < k: the weight of its expert from that expert's logit zj, in fp32 (the
-// exponentials within 2 ulp, one division: 4e-6 of the weight at most, which scales a
-// bf16 output); z and zmax (the softmax's reference) are the token's. Where the weights
-// are divided by their sum, a common factor is free: the softmax takes the largest
-// chosen logit as its reference, and scores of logits so small that fp32 would lose
-// them (sigmoid(z) = e^z, sqrt-softplus(z) = e^(z/2) there, to 1e-34) are taken
-// relative to the largest one's.
+// A chosen expert's score in fp32, within 2 ulp of the exponential and 1 of the rest:
+// sqrt-softplus(z) is e^(z/2) to 3e-8 below -16, which is a number long after e^z is none.
+__device__ __forceinline__ float chosen_score(float z, int fn) {
+    return fn == MOE_SCORE_SQRT_SOFTPLUS && z < -16.f ? expf(0.5f * z) : score_value(z, fn);
+}
+
+// Lane j < k: the weight of its expert from that expert's logit zj, in fp32 (4e-6 of the
+// weight at most, which scales a bf16 output); z and zmax (the softmax's reference) are
+// the token's. Where the weights are divided by their sum, a common factor is free: the
+// softmax takes the largest chosen logit as its reference, and so do the others where
+// that is below -20: sigmoid(z) = e^z and sqrt-softplus(z) = e^(z/2) there, to 2e-9, and
+// the ratios to the largest stay numbers down to 1e-30. The difference of two logits
+// is taken with its rounding's remainder.
 __device__ __forceinline__ float weight_of(const SelectArgs& a, int fn, const float (&z)[Q],
                                            float zmax, float zj) {
     float s;
     if (a.renorm) {
         const float zc = warp_max_value(zj);
-        if (fn == MOE_SCORE_SOFTMAX)
+        if (fn == MOE_SCORE_SOFTMAX) {
             s = zc > -INFINITY ? expf(zj - zc) : 0.f;
-        else if (zc < -80.f)
-            s = zc > -INFINITY ? expf(fn == MOE_SCORE_SIGMOID ? zj - zc : 0.5f * (zj - zc)) : 0.f;
-        else
-            s = score_value(zj, fn);
+        } else if (zc < -20.f) {
+            const float d = zj - zc, v = d - zj, left = (zj - (d - v)) - (zc + v);
+            const float half = fn == MOE_SCORE_SIGMOID ? 1.f : 0.5f, e = expf(half * d);
+            s = zj > -INFINITY ? fmaf(e, half * left, e) : 0.f;
+        } else {
+            s = chosen_score(zj, fn);
+        }
         const float den = warp_sum(s);
         return den > 0.f ? a.scale * __fdividef(s, den) : 0.f;
     }
-    if (fn != MOE_SCORE_SOFTMAX) return a.scale * score_value(zj, fn);
+    if (fn != MOE_SCORE_SOFTMAX) return a.scale * chosen_score(zj, fn);
     float part = 0.f;
 #pragma unroll
     for (int q = 0; q < Q; ++q) part += expf(z[q] - zmax);  // 0 for an expert that is out
