@@ -102,7 +102,8 @@ router_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restri
         // the weight vectors of the next column step are in flight while the
         // current ones are used
         uint4 cur[EPW];
-        load_w(cur, wg, e_base, E, d, kc + lane * 8);
+        // (a chunk of 128 columns has none for the upper lanes: past the last row's end)
+        if (lane * 8 < kw) load_w(cur, wg, e_base, E, d, kc + lane * 8);
         for (int c = lane * 8; c < kw; c += 256) {
             uint4 nxt[EPW];
             if (c + 256 < kw) load_w(nxt, wg, e_base, E, d, kc + c + 256);
