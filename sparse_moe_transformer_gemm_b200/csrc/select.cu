@@ -29,8 +29,9 @@
 // is 56 to 60% busy, and a warp waits mostly for fixed latencies and its turn; the
 // launch and the last tokens are the rest. Measured, E = 256, top-8, T = 16384, back
 // to back: 13.0 us without a bias or groups (reading the logits takes 2.6); biased, E =
-// 192 17.1 us; biased, 4 of 8 groups by their two best 25.6 us, of which 4 are the
-// latency of tokens with an open group. T = 64: 2.8 us, the launch's.
+// 192 17.1 us; biased, 4 of 8 groups by their two best 25 to 29.5 us by the inputs, of
+// which 4 and more are the latency of tokens with an open group. T = 64: 2.8 us, the
+// launch's.
 #include <float.h>
 
 #include "common.cuh"
